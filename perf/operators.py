@@ -10,8 +10,8 @@ Formats.  MXFP4: 32 consecutive values share a power of two 2^(byte - 127),
 elements are E2M1 nibbles, element 2j in the low nibble of byte j.  NVFP4: 16
 values share an E4M3 scale, times one fp32 scale of the tensor.  A cache page
 is one run of bytes with four sections: K codes [heads, page, dim / 2], V codes
-[heads, page / 16, dim / 2, 16], K scales [heads, page, dim / 32], V scales
-[heads, page / 16, dim / 32, 16]; the last axis of V's sections counts tokens.
+[heads, page / 16, dim / 2, 16], then K's and V's scales, each [heads, page / 16,
+dim / 32, 16]; where the last axis is 16 it counts tokens.
 """
 import math
 
@@ -205,9 +205,9 @@ def prepare(case, seed):
     cache = torch.empty(pages, at[4], device=DEVICE, dtype=torch.uint8)
     spikes = 1 + 3 * (torch.rand(heads, 1, dim, generator=g, device=DEVICE) < 0.03).float()  # a few strong channels, as keys have
     code, byte = mx_quantize((normal(g, pages, heads, page, dim) * spikes).bfloat16().float())
-    cache[:, at[0]:at[1]], cache[:, at[2]:at[3]] = pack(code).flatten(1), byte.flatten(1)
-    code, byte = mx_quantize(normal(g, pages, heads, page, dim).bfloat16().float())
     blocks = (pages, heads, page // 16, 16, -1)
+    cache[:, at[0]:at[1]], cache[:, at[2]:at[3]] = pack(code).flatten(1), byte.view(blocks).mT.flatten(1)
+    code, byte = mx_quantize(normal(g, pages, heads, page, dim).bfloat16().float())
     cache[:, at[1]:at[2]], cache[:, at[3]:] = pack(code).view(blocks).mT.flatten(1), byte.view(blocks).mT.flatten(1)
     state["q"] = normal(g, seqs, case["tokens"], case["q_heads"], dim).bfloat16()
     state["table"] = torch.randperm(pages, generator=g, device=DEVICE).int().view(seqs, width)
@@ -243,7 +243,7 @@ def plain_cache(st):
     seqs, width = st["table"].shape
     flat = (seqs, heads, width * page)
     part = rows[..., at[0]:at[1]].view(seqs, width, heads, page, dim // 2).transpose(1, 2)
-    s = power(rows[..., at[2]:at[3]].view(seqs, width, heads, page, dim // 32).transpose(1, 2))
+    s = power(rows[..., at[2]:at[3]].view(seqs, width, heads, page // 16, dim // 32, 16).mT.transpose(1, 2)).reshape(seqs, heads, width, page, -1)
     k = (e2m1_value(unpack(part)).unflatten(-1, (-1, 32)) * s[..., None]).reshape(*flat, dim)
     part = rows[..., at[1]:at[2]].view(seqs, width, heads, page // 16, dim // 2, 16).mT.transpose(1, 2)
     s = power(rows[..., at[3]:].view(seqs, width, heads, page // 16, dim // 32, 16).mT.transpose(1, 2))
@@ -297,7 +297,7 @@ def append(st):
     code, byte = mx_quantize(st["k"].float())
     k_value = (e2m1_value(code).unflatten(-1, (-1, 32)) * power(byte)[..., None]).flatten(-2).bfloat16()
     cache[:, at[0]:at[1]].view(-1, heads, page, dim // 2)[where, :, inside] = pack(code)
-    cache[:, at[2]:at[3]].view(-1, heads, page, dim // 32)[where, :, inside] = byte
+    cache[:, at[2]:at[3]].view(-1, heads, page // 16, dim // 32, 16)[where, :, inside // 16, :, inside % 16] = byte
     code, byte = mx_quantize(st["v"].float())
     v_value = (e2m1_value(code).unflatten(-1, (-1, 32)) * power(byte)[..., None]).flatten(-2).bfloat16()
     cache[:, at[1]:at[2]].view(-1, heads, page // 16, dim // 2, 16)[where, :, inside // 16, :, inside % 16] = pack(code)
@@ -376,7 +376,7 @@ def exact(case, seed):
             continue
         held = st["cache"][st["table"][b, : -(-n // page)].long()]
         kc, vc, ks, vs = held.split([code_bytes, code_bytes, scale_bytes, scale_bytes], 1)
-        kc, ks = kc.reshape(-1, heads, page, dim // 2), ks.reshape(-1, heads, page, dim // 32)
+        kc, ks = kc.reshape(-1, heads, page, dim // 2), ks.reshape(-1, heads, page // 16, dim // 32, 16).transpose(3, 4).reshape(-1, heads, page, dim // 32)
         vc = vc.reshape(-1, heads, page // 16, dim // 2, 16).transpose(3, 4).reshape(-1, heads, page, dim // 2)
         vs = vs.reshape(-1, heads, page // 16, dim // 32, 16).transpose(3, 4).reshape(-1, heads, page, dim // 32)
         pair = []
