@@ -23,6 +23,11 @@ Entry points (names follow the C ABI):
           nvfp4_quantize_noalloc(x)                            no workspace
           nvfp4_quantize_grouped(xs, groups, n_groups)         shared global scales
           prepare_nvfp4_grouped(xs, groups, n_groups).run()    table built once
+  Decode  mxfp4_matvec(x, q, s), nvfp4_matvec(x, q, s, g)      x W^T, 4-bit weights
+          mxfp4_kv_cache(layers, pages, kv_heads, head_dim)    paged 4-bit key/value cache
+          mxfp4_kv_append(cache, k, v, slots, page_size)       quantize into its pages
+          mxfp4_kv_attention(q, cache, page_table, lengths, ...) attention over it
+          mxfp4_kv_copy_pages(cache, src, dst), KVPagePool     copy, fork, compact, free
 and the adapter-level helpers of the MXFP8 export path ("PR #1935 完整报告",
 实现拆解 item 1 and 关键源码片段):
   mxfp8_quantize(weight) -> (qweight, scale)     flattens leading dims to 2-D
@@ -83,6 +88,13 @@ SIGNATURES = {
     "mxq_quantize_rowwise_grouped_plan": (ctypes.c_int, [_vp, _vp, _sz, _vp]),
     "nvfp4_grouped_plan_build": (ctypes.c_int, [_vp, _i32, _i32, _vp, _vp, _sz]),
     "nvfp4_quantize_grouped_plan": (ctypes.c_int, [_vp, _vp, _vp, _sz, _vp]),
+    "mxfp4_matvec": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, ctypes.c_int, _vp]),
+    "nvfp4_matvec": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, ctypes.c_int, _vp]),
+    "mxfp4_kv_page_bytes": (_sz, [_i32, _i32, _i32]),
+    "mxfp4_kv_append": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "mxfp4_kv_attention_workspace_size": (_sz, [_i32] * 7),
+    "mxfp4_kv_attention": (ctypes.c_int, [_vp, _vp, _vp]),
+    "mxfp4_kv_copy_pages": (ctypes.c_int, [_vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp]),
 }
 
 
@@ -103,6 +115,22 @@ class GroupedPlan(ctypes.Structure):
     _fields_ = [("kind", _i32), ("n_entries", _i32), ("n_groups", _i32), ("reserved", _i32),
                 ("total_tiles", _i64), ("table_bytes", ctypes.c_uint64),
                 ("workspace_bytes", ctypes.c_uint64)]
+
+
+class KVCacheDesc(ctypes.Structure):
+    """mxq_kv_cache."""
+    _fields_ = [("data", _vp), ("pages", _i64), ("page_stride", _i64), ("kv_heads", _i32),
+                ("head_dim", _i32), ("page_size", _i32), ("reserved", _i32)]
+
+
+class KVAttentionArgs(ctypes.Structure):
+    """mxq_kv_attention."""
+    _fields_ = [("q", _vp), ("q_seq_stride", _i64), ("q_token_stride", _i64),
+                ("q_head_stride", _i64), ("page_table", _vp), ("table_stride", _i64),
+                ("lengths", _vp), ("seqs", _i32), ("tokens", _i32), ("q_heads", _i32),
+                ("width", _i32), ("scale", ctypes.c_float), ("causal", _i32), ("window", _i32),
+                ("reserved", _i32), ("out", _vp), ("lse", _vp), ("workspace", _vp),
+                ("workspace_bytes", _sz)]
 
 
 class MXQError(RuntimeError):
@@ -678,3 +706,11 @@ def quantize_param(name: str, weight: torch.Tensor):
         raise ValueError(f"expected a weight parameter, got {name}")
     q, s = mxfp8_quantize(weight)
     return [(name, q), (name[: -len(".weight")] + ".weight_scale_inv", s)]
+
+
+# ---------------------------------------------------------------------------
+# decoding with 4-bit weights and a 4-bit key/value cache
+# ---------------------------------------------------------------------------
+
+from .decode import (KVPagePool, mxfp4_kv_append, mxfp4_kv_attention, mxfp4_kv_cache,  # noqa: E402
+                     mxfp4_kv_copy_pages, mxfp4_kv_page_bytes, mxfp4_matvec, nvfp4_matvec)

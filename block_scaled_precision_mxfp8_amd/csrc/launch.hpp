@@ -93,6 +93,12 @@ hipError_t launch_nvfp4_grouped(const NvEntry *table, const int32_t *starts, con
                                 int32_t n_groups, hipStream_t stream);
 int64_t nvfp4_tiles(int64_t rows, int64_t cols, int64_t *nseg);
 
+// Products of a few tokens with 4-bit weights; nv: NVFP4 (s E4M3, g) instead
+// of MXFP4 (s E8M0, g unused).  y bf16, or fp32 with out_f32.
+hipError_t launch_fp4_matvec(bool nv, const uint16_t *x, int64_t tokens, int64_t ldx,
+                             const uint8_t *q, const uint8_t *s, const float *g, int64_t n,
+                             int64_t k, void *y, int64_t ldy, bool out_f32, hipStream_t stream);
+
 hipError_t launch_nvfp4_dequant(const uint8_t *q, const uint8_t *s, const float *g,
                                 int64_t rows, int64_t cols, uint16_t *out, hipStream_t stream);
 

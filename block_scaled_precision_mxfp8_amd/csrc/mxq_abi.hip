@@ -10,6 +10,7 @@
 
 #include <vector>
 
+#include "kv4.hpp"
 #include "launch.hpp"
 #include "mxq.h"
 
@@ -223,6 +224,47 @@ mxq_status hand_over(const std::vector<unsigned char> &img, void *table_host, si
     if (!table_host) return MXQ_OK;
     if (bytes < img.size()) return MXQ_ESIZE;
     if (!img.empty()) memcpy(table_host, img.data(), img.size());
+    return MXQ_OK;
+}
+
+mxq_status fp4_matvec(bool nv, const uint16_t *x, int64_t tokens, int64_t ldx, const uint8_t *q,
+                      const uint8_t *s, const float *g, int64_t n, int64_t k, void *y, int64_t ldy,
+                      int out_fp32, void *stream)
+{
+    if (tokens < 0 || n < 0 || k < 0) return MXQ_EINVAL;
+    if (k % (nv ? 16 : 32) != 0) return MXQ_ESHAPE;
+    if (tokens == 0 || n == 0) return MXQ_OK;
+    if (!y || (nv && !g) || (k > 0 && (!x || !q || !s))) return MXQ_EINVAL;
+    if (ldx < k || ldy < n) return MXQ_ESHAPE;
+    if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(q, 4) || !aligned(g, 4) ||
+        !aligned(y, out_fp32 ? 4 : 2))
+        return MXQ_EALIGN;
+    if (!fits(tokens, ldx) || !fits(tokens, ldy) || !fits(n, k)) return MXQ_ESIZE;
+    return from_hip(mxq::launch_fp4_matvec(nv, x, tokens, ldx, q, s, g, n, k, y, ldy,
+                                           out_fp32 != 0, as_stream(stream)));
+}
+
+bool kv_shape_ok(int32_t heads, int32_t dim, int32_t page)
+{
+    return heads > 0 && (dim == 64 || dim == 96 || dim == 128 || dim == 192 || dim == 256) &&
+           page > 0 && page % 16 == 0 && page <= 65536;
+}
+
+// Checks a cache description (its data pointer only when it has pages).
+mxq_status check_kv(const mxq_kv_cache *c, mxq::Kv4Geom &geo)
+{
+    if (!c || c->pages < 0 || c->reserved != 0) return MXQ_EINVAL;
+    if (!kv_shape_ok(c->kv_heads, c->head_dim, c->page_size)) return MXQ_ESHAPE;
+    geo.pages = c->pages;
+    geo.page_stride = c->page_stride;
+    geo.heads = c->kv_heads;
+    geo.dim = c->head_dim;
+    geo.page = c->page_size;
+    if (c->pages == 0) return MXQ_OK;
+    if (!c->data) return MXQ_EINVAL;
+    if (c->page_stride < geo.page_bytes()) return MXQ_ESHAPE;
+    if (!aligned(c->data, 16) || c->page_stride % 16 != 0) return MXQ_EALIGN;
+    if (!fits(c->pages, c->page_stride)) return MXQ_ESIZE;
     return MXQ_OK;
 }
 
@@ -643,6 +685,135 @@ mxq_status nvfp4_dequantize(const uint8_t *q_packed, const uint8_t *s_e4m3,
     if (!fits(rows, cols)) return MXQ_ESIZE;
     return from_hip(mxq::launch_nvfp4_dequant(q_packed, s_e4m3, global_scale, rows, cols, out,
                                               as_stream(stream)));
+}
+
+mxq_status mxfp4_matvec(const uint16_t *x, int64_t tokens, int64_t ldx, const uint8_t *q,
+                        const uint8_t *scale, int64_t n, int64_t k, void *y, int64_t ldy,
+                        int out_fp32, void *stream)
+{
+    return fp4_matvec(false, x, tokens, ldx, q, scale, nullptr, n, k, y, ldy, out_fp32, stream);
+}
+
+mxq_status nvfp4_matvec(const uint16_t *x, int64_t tokens, int64_t ldx, const uint8_t *q,
+                        const uint8_t *s, const float *g, int64_t n, int64_t k, void *y,
+                        int64_t ldy, int out_fp32, void *stream)
+{
+    return fp4_matvec(true, x, tokens, ldx, q, s, g, n, k, y, ldy, out_fp32, stream);
+}
+
+size_t mxfp4_kv_page_bytes(int32_t kv_heads, int32_t head_dim, int32_t page_size)
+{
+    if (!kv_shape_ok(kv_heads, head_dim, page_size)) return 0;
+    return (size_t)mxq::Kv4Geom{0, 0, kv_heads, head_dim, page_size}.page_bytes();
+}
+
+mxq_status mxfp4_kv_append(const mxq_kv_cache *cache, const uint16_t *k, int64_t k_token_stride,
+                           int64_t k_head_stride, const uint16_t *v, int64_t v_token_stride,
+                           int64_t v_head_stride, const int64_t *slots, int64_t tokens,
+                           uint16_t *k_fq, uint16_t *v_fq, void *stream)
+{
+    mxq::Kv4Geom geo;
+    if (tokens < 0) return MXQ_EINVAL;
+    const mxq_status st = check_kv(cache, geo);
+    if (st != MXQ_OK) return st;
+    if (tokens == 0) return MXQ_OK;
+    if (!k || !v || !slots || !k_fq != !v_fq) return MXQ_EINVAL;
+    if (k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0)
+        return MXQ_EINVAL;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8) || !aligned(k_fq, 16) ||
+        !aligned(v_fq, 16) || k_token_stride % 8 || k_head_stride % 8 || v_token_stride % 8 ||
+        v_head_stride % 8)
+        return MXQ_EALIGN;
+    if (!fits(tokens, (int64_t)geo.heads * geo.dim) || !fits(tokens, k_token_stride) ||
+        !fits(tokens, v_token_stride))
+        return MXQ_ESIZE;
+    return from_hip(mxq::launch_kv4_append(geo, cache->data, k, k_token_stride, k_head_stride, v,
+                                           v_token_stride, v_head_stride, slots, tokens, k_fq,
+                                           v_fq, as_stream(stream)));
+}
+
+size_t mxfp4_kv_attention_workspace_size(int32_t seqs, int32_t tokens, int32_t q_heads,
+                                         int32_t kv_heads, int32_t head_dim, int32_t page_size,
+                                         int32_t width)
+{
+    if (seqs <= 0 || tokens <= 0 || q_heads <= 0 || width <= 0 ||
+        !kv_shape_ok(kv_heads, head_dim, page_size) || q_heads % kv_heads)
+        return 0;
+    const int32_t splits =
+        mxq::kv4_attention_splits(seqs, tokens, q_heads, kv_heads, head_dim, page_size, width);
+    if (splits <= 1) return 0;
+    return (size_t)splits * seqs * tokens * q_heads * (head_dim + 2) * sizeof(float);
+}
+
+mxq_status mxfp4_kv_attention(const mxq_kv_cache *cache, const mxq_kv_attention *args,
+                              void *stream)
+{
+    mxq::Kv4Attn a{};
+    if (!args || args->reserved != 0) return MXQ_EINVAL;
+    if (args->seqs < 0 || args->tokens < 0 || args->q_heads <= 0 || args->width < 0 ||
+        args->window < 0 || args->q_seq_stride < 0 || args->q_token_stride < 0 ||
+        args->q_head_stride < 0)
+        return MXQ_EINVAL;
+    const mxq_status st = check_kv(cache, a.geo);
+    if (st != MXQ_OK) return st;
+    if (args->q_heads % a.geo.heads != 0) return MXQ_ESHAPE;
+    if (args->seqs == 0 || args->tokens == 0) return MXQ_OK;
+    if (!args->q || !args->lengths || !args->out || (args->width > 0 && !args->page_table))
+        return MXQ_EINVAL;
+    if (args->width > 0 && args->table_stride < args->width) return MXQ_ESHAPE;
+    if (!aligned(args->q, 16) || args->q_seq_stride % 8 || args->q_token_stride % 8 ||
+        args->q_head_stride % 8 || !aligned(args->page_table, 4) || !aligned(args->lengths, 4) ||
+        !aligned(args->out, 16) || !aligned(args->lse, 4) || !aligned(args->workspace, 16))
+        return MXQ_EALIGN;
+    const int64_t group = args->q_heads / a.geo.heads, most = (int64_t)1 << 30;
+    if ((int64_t)args->width * a.geo.page > most || args->window > most ||
+        args->tokens * group > most || !fits(args->seqs, args->q_seq_stride) ||
+        !fits(args->tokens, args->q_token_stride) || !fits(args->q_heads, args->q_head_stride) ||
+        !fits(args->seqs, args->table_stride))
+        return MXQ_ESIZE;
+    const size_t need =
+        mxfp4_kv_attention_workspace_size(args->seqs, args->tokens, args->q_heads, a.geo.heads,
+                                          a.geo.dim, a.geo.page, args->width);
+    if (need > 0 && !args->workspace) return MXQ_EINVAL;
+    if (args->workspace_bytes < need) return MXQ_ESIZE;
+    a.cache = cache->data;
+    a.q = args->q;
+    a.q_seq = args->q_seq_stride;
+    a.q_tok = args->q_token_stride;
+    a.q_head = args->q_head_stride;
+    a.table = args->page_table;
+    a.table_stride = args->table_stride;
+    a.lengths = args->lengths;
+    a.seqs = args->seqs;
+    a.tokens = args->tokens;
+    a.q_heads = args->q_heads;
+    a.width = args->width;
+    a.scale = args->scale;
+    a.causal = args->causal != 0;
+    a.window = args->window;
+    a.out = args->out;
+    a.lse = args->lse;
+    a.part = static_cast<float *>(args->workspace);
+    a.splits = need > 0 ? mxq::kv4_attention_splits(a.seqs, a.tokens, a.q_heads, a.geo.heads,
+                                                    a.geo.dim, a.geo.page, a.width)
+                        : 1;
+    return from_hip(mxq::launch_kv4_attention(a, as_stream(stream)));
+}
+
+mxq_status mxfp4_kv_copy_pages(uint8_t *cache, int64_t layers, int64_t layer_stride, int64_t pages,
+                               int64_t page_stride, int64_t page_bytes, const int32_t *src,
+                               const int32_t *dst, int64_t n, void *stream)
+{
+    if (layers < 0 || pages < 0 || page_bytes < 0 || n < 0 || layer_stride < 0) return MXQ_EINVAL;
+    if (layers == 0 || pages == 0 || page_bytes == 0 || n == 0) return MXQ_OK;
+    if (!cache || !src || !dst) return MXQ_EINVAL;
+    if (page_stride < page_bytes) return MXQ_ESHAPE;
+    if (!aligned(cache, 16) || layer_stride % 16 || page_stride % 16 || page_bytes % 16 ||
+        !aligned(src, 4) || !aligned(dst, 4))
+        return MXQ_EALIGN;
+    if (!fits(pages, page_stride) || !fits(layers, layer_stride)) return MXQ_ESIZE;
+    return from_hip(mxq::launch_kv4_copy(cache, layers, layer_stride, pages, page_stride,
+                                         page_bytes, src, dst, n, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -22,6 +22,10 @@
  *     FP8, NVFP4, and QARL training and export", deep review, "What looked
  *     solid"; the packed FP4 output shape [..., N/2] from the review of
  *     fp4_act_quant in miles PR #1372.
+ *   - The operators of a decode step on 4-bit data: products of a few tokens
+ *     with MXFP4 / NVFP4 weights, and a paged key/value cache in MXFP4 (the
+ *     groups of 32 of mxfp4_simulate_qat(kv, 32), miles PR #1372) with its
+ *     append, attention and page copies.
  *
  * Conventions for every entry point
  *   - Data pointers are DEVICE pointers owned by the caller.  The library
@@ -458,6 +462,131 @@ mxq_status nvfp4_quantize_grouped_plan(const mxq_grouped_plan *plan, float *glob
 mxq_status nvfp4_dequantize(const uint8_t *q_packed, const uint8_t *s_e4m3,
                             const float *global_scale, int64_t rows, int64_t cols,
                             uint16_t *out, void *stream);
+
+/*
+ * Products of a few tokens with 4-bit weights (a decode step's projections):
+ *   y[t, n] = sum_k x[t, k] * w[n, k], summed in fp32, rounded once
+ *   w[n, k] = E2M1(q) * 2^(scale - 127)   (mxfp4_quantize's output), or
+ *             E2M1(q) * E4M3(s) * g       (nvfp4_quantize's output)
+ *   x      [tokens, k] bf16, row stride ldx elements; 16-byte aligned, ldx % 8 == 0
+ *   q      [n, k/2] packed E2M1, contiguous, 4-byte aligned
+ *   scale  [n, k/32] E8M0, s [n, k/16] E4M3, contiguous, any alignment
+ *   g      one float (device)
+ *   y      [tokens, n] bf16, or fp32 when out_fp32 != 0, row stride ldy
+ *          elements, aligned to its element
+ * Shape: k % 32 == 0 (MXFP4) or k % 16 == 0 (NVFP4); any tokens and n >= 0;
+ * k == 0 writes zeros.  Made for up to 64 tokens, which read the weights once;
+ * more run in blocks of 64.  NaN and Inf in x, and NaN scales, reach the sums
+ * they belong to.  The order of summation depends on the shape alone.
+ */
+mxq_status mxfp4_matvec(const uint16_t *x, int64_t tokens, int64_t ldx, const uint8_t *q,
+                        const uint8_t *scale, int64_t n, int64_t k, void *y, int64_t ldy,
+                        int out_fp32, void *stream);
+mxq_status nvfp4_matvec(const uint16_t *x, int64_t tokens, int64_t ldx, const uint8_t *q,
+                        const uint8_t *s, const float *g, int64_t n, int64_t k, void *y,
+                        int64_t ldy, int out_fp32, void *stream);
+
+/*
+ * A key/value cache held in MXFP4, in pages.  One layer of it is a device
+ * buffer of `pages` pages, page_stride bytes apart (16-byte aligned, a
+ * multiple of 16, at least mxfp4_kv_page_bytes).  A page is a run of bytes
+ * that holds page_size tokens of every head in four sections, one after the
+ * other:
+ *   K codes   [kv_heads][page_size][head_dim/2]          as mxfp4_quantize packs a row
+ *   V codes   [kv_heads][page_size/16][head_dim/2][16]   byte b of 16 tokens together
+ *   K scales  [kv_heads][page_size/16][head_dim/32][16]  E8M0
+ *   V scales  [kv_heads][page_size/16][head_dim/32][16]  E8M0
+ * Scales and codes are those of mxfp4_quantize over a token's head_dim values.
+ * Shape: head_dim 64, 96, 128, 192 or 256; page_size a multiple of 16, at most
+ * 65536 (MXQ_ESHAPE otherwise).
+ */
+typedef struct mxq_kv_cache {
+    uint8_t *data; /* page 0 of the layer */
+    int64_t pages, page_stride;
+    int32_t kv_heads, head_dim, page_size;
+    int32_t reserved; /* set to 0 */
+} mxq_kv_cache;
+
+/* Bytes of one page; 0 for a shape the cache does not have. */
+size_t mxfp4_kv_page_bytes(int32_t kv_heads, int32_t head_dim, int32_t page_size);
+
+/*
+ * Quantizes the keys and values of `tokens` tokens into their places.
+ *   k, v    [tokens, kv_heads, head_dim] bf16, token and head strides in
+ *           elements (views of a fused projection's output are fine), 16-byte
+ *           aligned, strides multiples of 8
+ *   slots   int64 [tokens]: page * page_size + position in the page; a token
+ *           whose slot is negative or past the cache is not stored.  Two
+ *           tokens of one call must not have the same slot.
+ *   k_fq, v_fq  optional [tokens, kv_heads, head_dim] bf16, contiguous, 16-byte
+ *           aligned: the values the cache holds for them; both or neither
+ */
+mxq_status mxfp4_kv_append(const mxq_kv_cache *cache, const uint16_t *k, int64_t k_token_stride,
+                           int64_t k_head_stride, const uint16_t *v, int64_t v_token_stride,
+                           int64_t v_head_stride, const int64_t *slots, int64_t tokens,
+                           uint16_t *k_fq, uint16_t *v_fq, void *stream);
+
+/*
+ * Attention of `tokens` query tokens of each of `seqs` sequences over their
+ * cached tokens:
+ *   o = sum_j p_j V_j,  p = softmax over the visible j of scale * (q . K_j)
+ * q_heads is a multiple of kv_heads; query head h reads kv head
+ * h / (q_heads / kv_heads).  Sequence b has lengths[b] cached tokens, the new
+ * ones among them (clamped to 0 .. width * page_size); its token j is in page
+ * page_table[b, j / page_size].  Query t stands at position lengths[b] -
+ * tokens + t and sees position j when j < lengths[b], j <= its own position
+ * (causal != 0) and j > its own position - window (window > 0).  Tokens of a
+ * page index outside 0 .. pages - 1 are not seen by any query.  A query that
+ * sees nothing gets zeros and lse = -inf.  What masked places hold, NaN
+ * included, does not matter.
+ *   q           [seqs, tokens, q_heads, head_dim] bf16, strides in elements
+ *               (multiples of 8), 16-byte aligned
+ *   page_table  int32 [seqs, width], row stride table_stride
+ *   lengths     int32 [seqs]
+ *   out         [seqs, tokens, q_heads, head_dim] bf16, contiguous, 16-byte aligned
+ *   lse         optional fp32 [seqs, tokens, q_heads]: the natural logarithm of
+ *               the sum of exp(score) over the visible tokens
+ *   workspace   >= mxfp4_kv_attention_workspace_size(...) bytes, 16-byte
+ *               aligned, no initial contents needed; may be NULL when that is 0
+ * Scores, maxima, sums and accumulators are fp32; softmax weights are rounded
+ * to bf16 for the product with V.  Magnitudes below 2^-126 may count as zero.
+ * width * page_size is at most 2^30, and window at most 2^30.
+ */
+typedef struct mxq_kv_attention {
+    const uint16_t *q;
+    int64_t q_seq_stride, q_token_stride, q_head_stride;
+    const int32_t *page_table;
+    int64_t table_stride;
+    const int32_t *lengths;
+    int32_t seqs, tokens, q_heads, width;
+    float scale;
+    int32_t causal, window;
+    int32_t reserved; /* set to 0 */
+    uint16_t *out;
+    float *lse;
+    void *workspace;
+    size_t workspace_bytes;
+} mxq_kv_attention;
+
+size_t mxfp4_kv_attention_workspace_size(int32_t seqs, int32_t tokens, int32_t q_heads,
+                                         int32_t kv_heads, int32_t head_dim, int32_t page_size,
+                                         int32_t width);
+
+mxq_status mxfp4_kv_attention(const mxq_kv_cache *cache, const mxq_kv_attention *args,
+                              void *stream);
+
+/*
+ * Copies pages inside a cache, all layers in one launch (a fork's last page,
+ * a compaction's moves): for every layer l and i < n, page dst[i] becomes a
+ * copy of page src[i].
+ *   cache  layers layer_stride bytes apart (a multiple of 16), pages as above
+ *   src, dst  int32 [n] on the device; a pair with an index outside
+ *          0 .. pages - 1 is left out.  No page may be in dst twice, nor be in
+ *          dst and, in another pair, in src.
+ */
+mxq_status mxfp4_kv_copy_pages(uint8_t *cache, int64_t layers, int64_t layer_stride, int64_t pages,
+                               int64_t page_stride, int64_t page_bytes, const int32_t *src,
+                               const int32_t *dst, int64_t n, void *stream);
 
 #ifdef __cplusplus
 }

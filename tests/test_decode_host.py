@@ -1,0 +1,247 @@
+"""The decode operators on the host (no GPU): the C entry points refuse bad
+arguments before launching anything, the binding refuses bad tensors, and the
+page pool's bookkeeping."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_precision_mxfp8_amd as mxq
+import decode_ref as ref
+
+P16, P8, P2, P1 = (ctypes.c_void_p(0x10000 + d) for d in (0, 8, 2, 1))  # never dereferenced
+NULL = None
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return mxq.load()
+
+
+def test_matvec_refusals(lib):
+    for nv in (False, True):
+        def f(x, t, ldx, q, s, n, k, y, ldy, f32=0, g=P16):
+            return lib.nvfp4_matvec(x, t, ldx, q, s, g, n, k, y, ldy, f32, NULL) if nv else \
+                lib.mxfp4_matvec(x, t, ldx, q, s, n, k, y, ldy, f32, NULL)
+
+        assert f(P16, -1, 64, P16, P16, 4, 64, P16, 4) == mxq.MXQ_EINVAL
+        assert f(P16, 1, 64, P16, P16, -4, 64, P16, 4) == mxq.MXQ_EINVAL
+        assert f(P16, 1, 64, P16, P16, 4, -64, P16, 4) == mxq.MXQ_EINVAL
+        assert f(P16, 1, 72, P16, P16, 4, 72, P16, 4) == mxq.MXQ_ESHAPE
+        assert f(NULL, 1, 64, P16, P16, 4, 64, P16, 4) == mxq.MXQ_EINVAL
+        assert f(P16, 1, 64, NULL, P16, 4, 64, P16, 4) == mxq.MXQ_EINVAL
+        assert f(P16, 1, 64, P16, NULL, 4, 64, P16, 4) == mxq.MXQ_EINVAL
+        assert f(P16, 1, 64, P16, P16, 4, 64, NULL, 4) == mxq.MXQ_EINVAL
+        assert f(P16, 1, 32, P16, P16, 4, 64, P16, 4) == mxq.MXQ_ESHAPE
+        assert f(P16, 1, 64, P16, P16, 4, 64, P16, 3) == mxq.MXQ_ESHAPE
+        assert f(P8, 1, 64, P16, P16, 4, 64, P16, 4) == mxq.MXQ_EALIGN
+        assert f(P16, 1, 68, P16, P16, 4, 64, P16, 4) == mxq.MXQ_EALIGN
+        assert f(P16, 1, 64, P2, P16, 4, 64, P16, 4) == mxq.MXQ_EALIGN
+        assert f(P16, 1, 64, P16, P16, 4, 64, P1, 4) == mxq.MXQ_EALIGN
+        assert f(P16, 1, 64, P16, P16, 4, 64, P2, 4, f32=1) == mxq.MXQ_EALIGN
+        assert f(P16, 1 << 40, 1 << 40, P16, P16, 4, 64, P16, 4) == mxq.MXQ_ESIZE
+        assert f(NULL, 0, 0, NULL, NULL, 4, 64, NULL, 0, g=NULL) == mxq.MXQ_OK
+        assert f(NULL, 1, 64, NULL, NULL, 0, 64, NULL, 0, g=NULL) == mxq.MXQ_OK
+    assert lib.nvfp4_matvec(P16, 1, 64, P16, P16, NULL, 4, 64, P16, 4, 0, NULL) == mxq.MXQ_EINVAL
+    assert lib.nvfp4_matvec(P16, 1, 48, P16, P16, P2, 4, 48, P16, 4, 0, NULL) == mxq.MXQ_EALIGN
+    assert lib.mxfp4_matvec(P16, 1, 48, P16, P16, 4, 48, P16, 4, 0, NULL) == mxq.MXQ_ESHAPE
+
+
+def desc(**kw):
+    d = dict(data=P16, pages=4, page_stride=8 * 64 * (128 + 8), kv_heads=8, head_dim=128, page_size=64, reserved=0)
+    d.update(kw)
+    return ctypes.byref(mxq.KVCacheDesc(**d))
+
+
+BAD_CACHES = [(dict(pages=-1), mxq.MXQ_EINVAL), (dict(reserved=1), mxq.MXQ_EINVAL), (dict(data=None), mxq.MXQ_EINVAL),
+              (dict(head_dim=80), mxq.MXQ_ESHAPE), (dict(head_dim=0), mxq.MXQ_ESHAPE), (dict(kv_heads=0), mxq.MXQ_ESHAPE),
+              (dict(page_size=24), mxq.MXQ_ESHAPE), (dict(page_size=0), mxq.MXQ_ESHAPE), (dict(page_size=1 << 17), mxq.MXQ_ESHAPE),
+              (dict(page_stride=8 * 64 * 136 - 16), mxq.MXQ_ESHAPE), (dict(page_stride=8 * 64 * 136 + 8), mxq.MXQ_EALIGN),
+              (dict(data=P8), mxq.MXQ_EALIGN), (dict(pages=1 << 50, page_stride=1 << 40), mxq.MXQ_ESIZE)]
+
+
+def test_page_bytes(lib):
+    for geo in ((8, 128, 64), (1, 64, 16), (3, 96, 48), (2, 256, 128), (5, 192, 32)):
+        assert mxq.mxfp4_kv_page_bytes(*geo) == ref.page_bytes(*geo) == lib.mxfp4_kv_page_bytes(*geo)
+    assert lib.mxfp4_kv_page_bytes(8, 100, 64) == 0 and lib.mxfp4_kv_page_bytes(8, 128, 8) == 0
+    with pytest.raises(ValueError):
+        mxq.mxfp4_kv_page_bytes(8, 100, 64)
+
+
+def test_append_refusals(lib):
+    def f(c, k=P16, kt=1024, kh=128, v=P16, vt=1024, vh=128, slots=P16, n=3, kq=NULL, vq=NULL):
+        return lib.mxfp4_kv_append(c, k, kt, kh, v, vt, vh, slots, n, kq, vq, NULL)
+
+    for kw, status in BAD_CACHES:
+        assert f(desc(**kw)) == status, kw
+    assert f(NULL) == mxq.MXQ_EINVAL
+    assert f(desc(), n=-1) == mxq.MXQ_EINVAL
+    for kw in (dict(k=NULL), dict(v=NULL), dict(slots=NULL), dict(kq=P16), dict(vq=P16), dict(kt=-8), dict(vh=-8)):
+        assert f(desc(), **kw) == mxq.MXQ_EINVAL, kw
+    for kw in (dict(k=P8), dict(v=P8), dict(slots=ctypes.c_void_p(0x10004)), dict(kt=1028), dict(vh=4), dict(kq=P8, vq=P16)):
+        assert f(desc(), **kw) == mxq.MXQ_EALIGN, kw
+    assert f(desc(), n=1 << 60) == mxq.MXQ_ESIZE
+    assert f(desc(), k=NULL, v=NULL, slots=NULL, n=0) == mxq.MXQ_OK
+
+
+def test_attention_refusals(lib):
+    ok = dict(q=P16, q_seq_stride=4096, q_token_stride=4096, q_head_stride=128, page_table=P16, table_stride=4, lengths=P16, seqs=2,
+              tokens=1, q_heads=32, width=4, scale=0.1, causal=1, window=0, reserved=0, out=P16, lse=None, workspace=P16,
+              workspace_bytes=1 << 40)
+
+    def f(c, **kw):
+        return lib.mxfp4_kv_attention(c, ctypes.byref(mxq.KVAttentionArgs(**{**ok, **kw})), NULL)
+
+    for kw, status in BAD_CACHES:
+        assert f(desc(**kw)) == status, kw
+    assert f(NULL) == mxq.MXQ_EINVAL and lib.mxfp4_kv_attention(desc(), NULL, NULL) == mxq.MXQ_EINVAL
+    for kw in (dict(seqs=-1), dict(tokens=-1), dict(q_heads=0), dict(width=-1), dict(window=-1), dict(q=None), dict(page_table=None),
+               dict(lengths=None), dict(out=None), dict(reserved=2), dict(q_head_stride=-128)):
+        assert f(desc(), **kw) == mxq.MXQ_EINVAL, kw
+    assert f(desc(), q_heads=12) == mxq.MXQ_ESHAPE
+    assert f(desc(), table_stride=3) == mxq.MXQ_ESHAPE
+    for kw in (dict(q=P8), dict(q_token_stride=4), dict(page_table=P2), dict(lengths=P2), dict(out=P8), dict(lse=P2), dict(workspace=P8)):
+        assert f(desc(), **kw) == mxq.MXQ_EALIGN, kw
+    assert f(desc(), width=1 << 25, table_stride=1 << 25) == mxq.MXQ_ESIZE
+    assert f(desc(), window=(1 << 30) + 1) == mxq.MXQ_ESIZE
+    assert f(desc(), seqs=0, q=None, out=None) == mxq.MXQ_OK
+    assert f(desc(), tokens=0, q=None, out=None) == mxq.MXQ_OK
+    size = lib.mxfp4_kv_attention_workspace_size
+    need = size(1, 1, 32, 8, 128, 64, 1024)
+    assert need > 0
+    kw = dict(seqs=1, width=1024, table_stride=1024)
+    assert f(desc(), workspace_bytes=need - 1, **kw) == mxq.MXQ_ESIZE
+    assert f(desc(), workspace=None, **kw) == mxq.MXQ_EINVAL
+    assert size(0, 1, 32, 8, 128, 64, 4) == 0 and size(1, 1, 32, 5, 128, 64, 4) == 0 and size(1, 1, 32, 8, 80, 64, 4) == 0
+
+
+def test_copy_refusals(lib):
+    def f(c=P16, layers=2, ls=4096, pages=4, ps=1024, nbytes=1024, src=P16, dst=P16, n=2):
+        return lib.mxfp4_kv_copy_pages(c, layers, ls, pages, ps, nbytes, src, dst, n, NULL)
+
+    for kw in (dict(layers=-1), dict(pages=-1), dict(nbytes=-16), dict(n=-1), dict(ls=-16), dict(c=NULL), dict(src=NULL), dict(dst=NULL)):
+        assert f(**kw) == mxq.MXQ_EINVAL, kw
+    assert f(ps=1008) == mxq.MXQ_ESHAPE
+    for kw in (dict(c=P8), dict(ls=4100), dict(ps=1032), dict(nbytes=1000), dict(src=P2), dict(dst=P2)):
+        assert f(**kw) == mxq.MXQ_EALIGN, kw
+    assert f(pages=1 << 50, ps=1 << 40) == mxq.MXQ_ESIZE
+    assert f(c=NULL, n=0) == f(c=NULL, layers=0) == f(c=NULL, pages=0) == mxq.MXQ_OK
+
+
+def test_binding_refuses_cpu_tensors_and_types():
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    q, s = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        mxq.mxfp4_matvec(x, q, s)
+    with pytest.raises(TypeError):
+        mxq.mxfp4_matvec(x.float(), q, s)
+    with pytest.raises(TypeError):
+        mxq.nvfp4_matvec(x, q, s, torch.zeros(1, dtype=torch.float64))
+    with pytest.raises((TypeError, ValueError)):
+        mxq.mxfp4_kv_append(q, x.view(1, 2, 64), x.view(1, 2, 64), torch.zeros(1, dtype=torch.int64), 16)
+    with pytest.raises((TypeError, ValueError)):
+        mxq.mxfp4_kv_attention(x.view(1, 1, 2, 64), q, torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), 1, 16)
+    with pytest.raises(TypeError):
+        mxq.mxfp4_kv_copy_pages(q.float(), torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        mxq.mxfp4_kv_copy_pages(q, torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+# -- the page pool ----------------------------------------------------------------
+
+def check(pool, held):
+    """Reference counts, free pages and tables agree; each sequence reads back
+    the tokens in ``held`` = (store {slot: token}, {seq: [tokens]})."""
+    store, seqs = held
+    counts = [0] * len(pool.refs)
+    for name, tokens in seqs.items():
+        pages = pool.pages(name)
+        assert pool.length(name) == len(tokens) and len(pages) == -(-len(tokens) // pool.page_size)
+        for p in pages:
+            counts[p] += 1
+        for i, t in enumerate(tokens):
+            assert store[pages[i // pool.page_size], i % pool.page_size] == t
+    assert counts == pool.refs and pool.free_pages == counts.count(0)
+
+
+def copy(store, size, src, dst):
+    assert len(set(dst)) == len(dst) and not set(src) & set(dst)
+    for s, d in zip(src, dst):
+        for i in range(size):
+            store[d, i] = store.get((s, i))
+
+
+def test_pool_against_a_model():
+    """Random extends, forks, truncations, frees and compactions."""
+    rng = np.random.default_rng(1)
+    size = 4
+    pool = mxq.KVPagePool(40, size)
+    store, seqs, fresh = {}, {}, 0
+    for step in range(600):
+        what = rng.choice(["extend", "extend", "extend", "fork", "truncate", "free", "compact"])
+        names = list(seqs)
+        if what == "extend":
+            name = names[rng.integers(len(names))] if names and rng.random() < 0.8 else ("s", step)
+            n = int(rng.integers(0, 9))
+            before = (list(pool.refs), pool.free_pages)
+            try:
+                slots, src, dst = pool.extend(name, n)
+            except MemoryError:
+                assert (list(pool.refs), pool.free_pages) == before
+                continue
+            copy(store, size, src, dst)
+            assert len(slots) == n and len(set(slots)) == n
+            seqs.setdefault(name, [])
+            for slot in slots:
+                store[slot // size, slot % size] = fresh
+                seqs[name].append(fresh)
+                fresh += 1
+        elif what == "fork" and names:
+            pool.fork(names[0], ("f", step))
+            seqs[("f", step)] = list(seqs[names[0]])
+        elif what == "truncate" and names:
+            name = names[rng.integers(len(names))]
+            n = int(rng.integers(0, len(seqs[name]) + 1))
+            pool.truncate(name, n)
+            del seqs[name][n:]
+        elif what == "free" and names:
+            name = names[rng.integers(len(names))]
+            pool.free(name)
+            del seqs[name]
+            assert name not in pool
+        elif what == "compact":
+            copy(store, size, *pool.compact())
+            assert 0 not in pool.refs[:sum(r > 0 for r in pool.refs)]
+        check(pool, (store, seqs))
+
+
+def test_pool_tables_and_refusals():
+    pool = mxq.KVPagePool(6, 16)
+    assert pool.extend("a", 20) == (list(range(20)), [], [])
+    pool.extend("b", 3)
+    pool.fork("a", "c")
+    slots, src, dst = pool.extend("c", 1)
+    assert (slots, src, dst) == ([3 * 16 + 4], [1], [3])
+    table, lengths = pool.table(["c", "b"])
+    assert table.tolist() == [[0, 3], [2, -1]] and lengths.tolist() == [21, 3]
+    assert table.dtype == lengths.dtype == torch.int32
+    assert pool.table(["b"], width=3)[0].tolist() == [[2, -1, -1]] and pool.table([])[0].shape == (0, 0)
+    with pytest.raises(ValueError):
+        pool.table(["a"], width=1)
+    with pytest.raises(MemoryError):
+        pool.extend("d", 100)
+    assert "d" not in pool
+    with pytest.raises(ValueError):
+        pool.fork("a", "c")
+    with pytest.raises(ValueError):
+        pool.truncate("a", 21)
+    with pytest.raises(ValueError):
+        pool.extend("a", -1)
+    with pytest.raises(KeyError):
+        pool.free("nobody")
+    pool.free("b")
+    assert pool.compact() == ([3], [2])
+    assert pool.table(["a", "c"])[0].tolist() == [[0, 1], [0, 2]]
+    with pytest.raises(ValueError):
+        mxq.KVPagePool(-1)
