@@ -5,53 +5,33 @@
 //
 // x bf16, q and s as the quantizers write them, sums in fp32, y bf16 or fp32.
 //
-// Each wave multiplies 16-row strips of weights with up to 64 tokens on the
-// matrix cores (v_mfma_f32_16x16x32_bf16, weights as the A operand).  The
-// contraction runs over k, so any order of k serves as long as both operands
-// agree: lane (m, kg) = (lane % 16, lane / 16) loads the 16 contiguous code
-// bytes of row m, k = 32 kg .. 32 kg + 31 of a 128-wide chunk -- for MXFP4
-// exactly one scale group -- and the j-th of four matrix instructions takes
-// its j-th dword (8 elements).  A row's 64 bytes of a chunk are contiguous
-// over the kg lanes, so codes come straight from row-major storage.
+// Both kernels multiply on the matrix cores (v_mfma_f32_16x16x32_bf16, weights
+// as the A operand, tokens as B); lane (m, kg) = (lane % 16, lane / 16) holds
+// 8 elements of row or column m.  The contraction may take k in any order as
+// long as both operands agree.
 //
-// MXFP4 weights are exact in bf16, and v_cvt_scalef32_pk_bf16_fp4 applies the
-// scale while it decodes: it reads only the exponent field of its scale
-// operand, so a rotated scale word serves without masking (checked for every
-// code and scale byte, junk in sign and fraction included).  NVFP4's E2M1 x
-// E4M3 has at most 6 significant bits, also exact in bf16; g multiplies the
-// fp32 sum.
+// MXFP4 weights are exact in bf16 and decoded with their scale by one
+// conversion for two.  NVFP4's E2M1 x E4M3 has at most 6 significant bits, also exact in bf16; g
+// multiplies the fp32 sum.
+//
+// What limits these kernels is how a wave's loads fall on cache lines: a
+// 16-byte-per-lane load costs about a clock for every line that a group of 16
+// neighbouring lanes touches.  Lane m holding row m, as the matrix cores want
+// it, touches 64 (measured: 72 clocks a load, 37 us for 64 tokens x [16384,
+// 7168]); four neighbouring lanes on 64 bytes of one row touch 16 (27 us).
 
+#include "fp4_mfma.hpp"
 #include "launch.hpp"
-#include "mxq_device.hpp"
 
 namespace mxq {
 
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-// 16 and 8 bytes from addresses aligned to 4 and 1
-struct __attribute__((packed, aligned(4))) Codes16 { uint32_t w[4]; };
-struct __attribute__((packed, aligned(1))) Bytes8 { uint32_t w[2]; };
-struct __attribute__((packed, aligned(1))) Bytes2 { uint16_t w; };
-
-__device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&d)[N], const uint8_t *p)
 {
-    return __builtin_bit_cast(bf16x8, make_uint4(a, b, c, d));
-}
-
-template <int kByte>
-__device__ __forceinline__ uint32_t mx_pair(uint32_t codes, float scale)
-{
-    return __builtin_bit_cast(uint32_t,
-                              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, kByte));
-}
-
-__device__ __forceinline__ bf16x8 mx_frag(uint32_t codes, float scale)
-{
-    return as_bf16x8(mx_pair<0>(codes, scale), mx_pair<1>(codes, scale), mx_pair<2>(codes, scale),
-                     mx_pair<3>(codes, scale));
+    const Bytes<4 * N> v = *reinterpret_cast<const Bytes<4 * N> *>(p);
+    __builtin_memcpy(d, &v, sizeof v);
 }
 
 template <int kByte>
@@ -61,166 +41,423 @@ __device__ __forceinline__ uint32_t nv_pair(uint32_t codes, float scale)
     return bf16x2_exact(v.x * scale, v.y * scale);
 }
 
-__device__ __forceinline__ bf16x8 nv_frag(uint32_t codes, float scale)
+// 8 weights.  Scale word: the E8M0 byte in bits 23..30, or the E4M3 byte kByte.
+template <bool kNV, int kByte>
+__device__ __forceinline__ bf16x8 weights8(uint32_t codes, uint32_t scale)
 {
-    return as_bf16x8(nv_pair<0>(codes, scale), nv_pair<1>(codes, scale), nv_pair<2>(codes, scale),
-                     nv_pair<3>(codes, scale));
+    if constexpr (kNV) {
+        const float f = __builtin_amdgcn_cvt_f32_fp8((int)scale, kByte);
+        return as_bf16x8(nv_pair<0>(codes, f), nv_pair<1>(codes, f), nv_pair<2>(codes, f),
+                         nv_pair<3>(codes, f));
+    } else {
+        return fp4_frag(codes, scale);
+    }
 }
 
-// One wave's share of RT strips of 16 rows and NT tiles of 16 tokens; the
-// workgroup's kWaves waves take the 256-wide steps of k in turn and add their
-// sums through LDS in a fixed order.
-template <bool kNV, int RT, int NT, int kWaves>
-__global__ __launch_bounds__(kWaves * 64) void fp4_matvec_kernel(
-    const uint16_t *__restrict__ x, int64_t tokens, int64_t ldx, const uint8_t *__restrict__ q,
-    const uint8_t *__restrict__ s, const float *__restrict__ g, int64_t n, int64_t k,
-    void *__restrict__ y, int64_t ldy, int out_f32)
+__device__ __forceinline__ void store_y(void *y, int64_t at, float v, int out_f32)
 {
-    constexpr int kGroup = kNV ? 16 : 32;
+    if (out_f32)
+        static_cast<float *>(y)[at] = v;
+    else
+        static_cast<__bf16 *>(y)[at] = (__bf16)v;
+}
+
+struct MatvecArgs {
+    const uint16_t *x;
+    int64_t tokens, ldx;
+    const uint8_t *q, *s;
+    const float *g;
+    int64_t n, k;
+    void *y;
+    int64_t ldy;
+    int out_f32;
+};
+
+// ---------------------------------------------------------------------------
+// Up to 4 tokens: the 16 rows of A are 4 weight rows x 4 slices of k, the 16
+// columns of B 4 tokens x the same 4 slices; of the product only the blocks of
+// equal slices are used, their sum over the slices is the result.  A quad of
+// lanes then reads 64 contiguous bytes of one row and lane (kg, a, p) = (lane
+// / 16, lane / 4 % 4, lane % 4) holds 16 of them, k = 128 kg + 32 p .. of a
+// step of 512: one MXFP4 group, and exactly what four products want, with no
+// exchange between lanes.  The matrix cores do four times the work needed,
+// still under the time of the loads.  The tokens sit in LDS, rows 16 bytes off
+// a multiple of 256 apart, so 16 lanes' reads fall on different banks.
+//
+// The waves of a workgroup take the steps of k in turn, kDepth of them
+// in flight; sums are added through LDS in a fixed order.
+// ---------------------------------------------------------------------------
+constexpr int64_t kFewLds = 72 << 10;  // two workgroups per CU at the least
+
+__host__ __device__ inline int64_t few_pitch(int64_t k) { return (k + 511) / 512 * 512 + 8; }
+
+template <bool kNV, int RS, int kWaves, int kDepth>
+__device__ __forceinline__ void few_body(const MatvecArgs &a, uint16_t *xs)
+{
+    constexpr int kGroup = kNV ? 16 : 32, kSb = 32 / kGroup;  // scale bytes per lane and step
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int m = lane & 15, kg = lane >> 4;
-    const int64_t row0 = (int64_t)blockIdx.x * (RT * 16);
-    const int64_t tok0 = (int64_t)blockIdx.y * (NT * 16);
+    const int kg = lane >> 4, row = (lane >> 2) & 3, p = lane & 3, piece = kg * 4 + p;
+    const int64_t row0 = (int64_t)blockIdx.x * (RS * 4);
+    const int tokens = (int)a.tokens, k = (int)a.k;
+    const int full = k / 512, steps = (k + 511) / 512;
 
-    const uint8_t *qrow[RT], *srow[RT];
-    const uint16_t *xrow[NT];
+    const uint8_t *qr[RS], *sr[RS];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {  // rows past the end repeat the last: their sums are dropped
-        const int64_t r = min(row0 + i * 16 + m, n - 1);
-        qrow[i] = q + r * (k >> 1) + kg * 16;
-        srow[i] = s + r * (k / kGroup);
+    for (int i = 0; i < RS; ++i) {  // rows past the end repeat the last: their sums are dropped
+        const int64_t r = min(row0 + 4 * i + row, a.n - 1);
+        qr[i] = a.q + r * (a.k >> 1) + piece * 16;
+        sr[i] = a.s + r * (a.k / kGroup) + piece * kSb;
+    }
+    const float gs = kNV ? *a.g : 1.0f;
+    struct Step { uint32_t w[RS][4], s[RS]; } ring[kDepth];
+    auto load = [&](Step &t, int st) {
+#pragma unroll
+        for (int i = 0; i < RS; ++i) {
+            const Words<4> v = *reinterpret_cast<const Words<4> *>(qr[i] + (int64_t)st * 256);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) t.w[i][j] = v.w[j];
+            const uint8_t *sp = sr[i] + (int64_t)st * (16 * kSb);
+            if constexpr (kNV) {
+                const Bytes<2> b = *reinterpret_cast<const Bytes<2> *>(sp);
+                t.s[i] = (uint32_t)b.b[0] | (uint32_t)b.b[1] << 8;
+            } else {
+                t.s[i] = *sp;
+            }
+        }
+    };
+    if (full > 0) {  // steps past the last repeat it, unused: no branch between the loads
+#pragma unroll
+        for (int u = 0; u < kDepth; ++u) load(ring[u], min(wave + u * kWaves, full - 1));
+    }
+
+    const int pitch = (int)few_pitch(k), width = steps * 64;  // 16-byte pieces of a row, padding included
+    for (int base = threadIdx.x; base < tokens * width; base += kWaves * kWave * 4) {
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int e = base + u * kWaves * kWave, t = e / width, c = (e - t * width) * 8;
+            v[u] = make_uint4(0, 0, 0, 0);
+            if (t < tokens && c < k) v[u] = ld16<false>(a.x + t * a.ldx + c);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int e = base + u * kWaves * kWave, t = e / width, c = (e - t * width) * 8;
+            if (t < tokens) *reinterpret_cast<uint4 *>(xs + t * pitch + c) = v[u];
+        }
+    }
+    const uint16_t *xl = xs + min(row, tokens - 1) * pitch + piece * 32;
+    __syncthreads();
+
+    f32x4 acc[RS];
+#pragma unroll
+    for (int i = 0; i < RS; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](const Step &t, int st) {
+        static_for<0, 4, 1>([&](auto J) {
+            constexpr int j = J;
+            const bf16x8 b = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(xl + st * 512 + 8 * j));
+#pragma unroll
+            for (int i = 0; i < RS; ++i)
+                acc[i] = mfma(weights8<kNV, j / 2>(t.w[i][j], kNV ? t.s[i] : t.s[i] << 23), b, acc[i]);
+        });
+    };
+    for (int base = wave; base < full; base += kDepth * kWaves) {
+        static_for<0, kDepth, 1>([&](auto U) {
+            const int st = base + U * kWaves;
+            if (st < full) {
+                multiply(ring[U], st);
+                if (st + kDepth * kWaves < full) load(ring[U], st + kDepth * kWaves);
+            }
+        });
+    }
+    if (full < steps && wave == full % kWaves) {  // a partial step: what lies past k counts as zero
+        const int valid = k - full * 512 - piece * 32;
+        Step &t = ring[0];
+#pragma unroll
+        for (int i = 0; i < RS; ++i) {
+            t.s[i] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                t.w[i][j] = 8 * j < valid ? reinterpret_cast<const Words<4> *>(qr[i] + (int64_t)full * 256)->w[j] : 0u;
+#pragma unroll
+            for (int j = 0; j < kSb; ++j)
+                if (kGroup * j < valid) t.s[i] |= (uint32_t)sr[i][(int64_t)full * (16 * kSb) + j] << (8 * j);
+        }
+        multiply(t, full);
+    }
+
+    // lane (kg, t, p) holds rows 4 kg + 0..3 of the product, slices p = 0..3 of
+    // weight row kg, in column (t, p)
+    __shared__ float red[kWaves][RS][16];
+#pragma unroll
+    for (int i = 0; i < RS; ++i) {
+        float v = p == 0 ? acc[i][0] : p == 1 ? acc[i][1] : p == 2 ? acc[i][2] : acc[i][3];
+        v += __uint_as_float(dpp_swap1(__float_as_uint(v)));
+        v += __uint_as_float(dpp_swap2(__float_as_uint(v)));
+        if (p == 0) red[wave][i][lane >> 2] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x < RS * 16) {
+        const int e = threadIdx.x, t = e & 3;
+        const int64_t r = row0 + (e >> 4) * 4 + ((e >> 2) & 3);
+        float v = red[0][e >> 4][e & 15];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v += red[w][e >> 4][e & 15];
+        if (t < tokens && r < a.n) store_y(a.y, t * a.ldy + r, v * gs, a.out_f32);
+    }
+}
+
+template <bool kNV, int RS, int kWaves, int kDepth>
+__global__ __launch_bounds__(kWaves * 64) void matvec_few_kernel(MatvecArgs a)
+{
+    extern __shared__ __align__(16) uint16_t few_xs[];
+    few_body<kNV, RS, kWaves, kDepth>(a, few_xs);
+}
+
+// ---------------------------------------------------------------------------
+// More tokens: RT strips of 16 rows by NT tiles of 16 tokens per workgroup,
+// whose waves split k in contiguous runs of chunks of 128.
+//
+// Loads have lane 4 r + p on the p-th 16 bytes of row (or token) r; ds_bpermute
+// then gives lane (m, kg) what lane 4 m + kg loaded.  For tokens that is the
+// operand (k = 32 j + 8 kg .. from the j-th load).  For weights it is piece kg
+// of row m, and a 4 x 4 transposition over kg (four permlane swaps) makes it
+// dword kg of piece j, the same k.  One scale load covers four chunks.  kDepth
+// chunks of weights, one of tokens are in flight.
+// ---------------------------------------------------------------------------
+
+// w[j] of lane group kg <- w[kg] of lane group j
+__device__ __forceinline__ void transpose_kg(uint32_t (&w)[4])
+{
+    auto r = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+    w[0] = r[0];
+    w[2] = r[1];
+    r = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+    w[1] = r[0];
+    w[3] = r[1];
+    r = __builtin_amdgcn_permlane16_swap(w[0], w[1], false, false);
+    w[0] = r[0];
+    w[1] = r[1];
+    r = __builtin_amdgcn_permlane16_swap(w[2], w[3], false, false);
+    w[2] = r[0];
+    w[3] = r[1];
+}
+
+__device__ __forceinline__ uint32_t from_lane(int lane4, uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_ds_bpermute(lane4, (int)v);
+}
+
+template <bool kNV, int RT, int NT, int kWaves, int kDepth>
+__device__ __forceinline__ void many_body(const MatvecArgs &a)
+{
+    constexpr int kGroup = kNV ? 16 : 32, SW = kNV ? 2 : 1;  // scale words per row and chunk
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int m = lane & 15, kg = lane >> 4, r4 = lane >> 2, p4 = lane & 3;
+    const int64_t row0 = (int64_t)blockIdx.x * (RT * 16), tok0 = (int64_t)blockIdx.y * (NT * 16);
+    const int64_t n = a.n, k = a.k;
+
+    // rows and tokens past the end repeat the last: their sums are dropped
+    const uint8_t *qr[RT], *sr[RT];
+    const uint16_t *xr[NT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int64_t r = min(row0 + i * 16 + r4, n - 1);
+        qr[i] = a.q + r * (k >> 1) + p4 * 16;
+        sr[i] = a.s + r * (k / kGroup) + p4 * (4 * SW);
     }
 #pragma unroll
-    for (int i = 0; i < NT; ++i) xrow[i] = x + min(tok0 + i * 16 + m, tokens - 1) * ldx + kg * 32;
+    for (int i = 0; i < NT; ++i) xr[i] = a.x + min(tok0 + i * 16 + r4, a.tokens - 1) * a.ldx + p4 * 8;
+
+    const float gs = kNV ? *a.g : 1.0f;
+    const int chunks = (int)(k / 128), per = (chunks + kWaves - 1) / kWaves;
+    const int c0 = wave * per, c1 = min(chunks, c0 + per), last = chunks - 1;
+    const int from_mk = 4 * (4 * m + kg), from_m = 16 * m;
 
     f32x4 acc[RT][NT];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < NT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // one chunk of 128 from its codes, scale bits and the tokens
-    auto chunk = [&](const Codes16(&w)[RT], const uint32_t(&sc)[RT], int64_t k0, int valid) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            bf16x8 b[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (8 * j < valid) v = *reinterpret_cast<const uint4 *>(xrow[t] + k0 + 8 * j);
-                b[t] = __builtin_bit_cast(bf16x8, v);
-            }
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                bf16x8 a;
-                if constexpr (kNV)
-                    a = nv_frag(w[i].w[j],
-                                j < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)sc[i], 0)
-                                      : __builtin_amdgcn_cvt_f32_fp8((int)sc[i], 1));
-                else
-                    a = mx_frag(w[i].w[j], __uint_as_float(sc[i]));
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[t], acc[i][t], 0, 0, 0);
-            }
-        }
-    };
-
-    const int64_t full = k / 256;
-    const int rot = (8 * kg + 9) & 31;  // scale byte kg of a word -> bits 23..30
-    for (int64_t step = wave; step < full; step += kWaves) {
-        const int64_t k0 = step * 256;
-        Codes16 w[2][RT];
-        uint32_t sc[2][RT];
+    uint32_t wb[kDepth][RT][4], sb[2][RT][SW];
+    uint4 xc[4][NT];
+    auto load_w = [&](uint32_t(&d)[RT][4], int c) {
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-            w[0][i] = *reinterpret_cast<const Codes16 *>(qrow[i] + (k0 >> 1));
-            w[1][i] = *reinterpret_cast<const Codes16 *>(qrow[i] + (k0 >> 1) + 64);
-            if constexpr (kNV) {
-                const uint8_t *p = srow[i] + (k0 >> 4) + 2 * kg;
-                sc[0][i] = reinterpret_cast<const Bytes2 *>(p)->w;
-                sc[1][i] = reinterpret_cast<const Bytes2 *>(p + 8)->w;
-            } else {
-                const Bytes8 b = *reinterpret_cast<const Bytes8 *>(srow[i] + (k0 >> 5));
-                sc[0][i] = __builtin_amdgcn_alignbit(b.w[0], b.w[0], rot);
-                sc[1][i] = __builtin_amdgcn_alignbit(b.w[1], b.w[1], rot);
-            }
+            const Words<4> v = *reinterpret_cast<const Words<4> *>(qr[i] + (int64_t)min(c, last) * 64);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[i][j] = v.w[j];
         }
-        chunk(w[0], sc[0], k0, 32);
-        chunk(w[1], sc[1], k0 + 128, 32);
+    };
+    auto load_s = [&](uint32_t(&d)[RT][SW], int c) {  // chunk c + p4
+        const int64_t at = (int64_t)(min(c + p4, last) - p4) * (4 * SW);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) load_words<SW>(d[i], sr[i] + at);
+    };
+    auto load_x = [&](int j, int c) {
+        const int64_t at = (int64_t)min(c, last) * 128 + 32 * j;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) xc[j][t] = ld16<false>(xr[t] + at);
+    };
+    if (c0 < c1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_x(j, c0);
+        load_s(sb[0], c0);
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) load_w(wb[d], c0 + d);
     }
-    if (full * 256 < k && wave == (int)(full % kWaves)) {  // the last, partial step
-        for (int64_t k0 = full * 256; k0 < k; k0 += 128) {
-            // what of this lane's 32 elements exists: 0, 16 (NVFP4) or 32
-            const int valid = (int)min((int64_t)32, max((int64_t)0, k - k0 - kg * 32));
-            Codes16 w[RT];
-            uint32_t sc[RT];
+    static_assert(8 % kDepth == 0, "ring positions are constants in the unrolled loop");
+    for (int base = c0; base < c1; base += 8) {
+        static_for<0, 8, 1>([&](auto U) {
+            constexpr int u = U;
+            const int c = base + u;
+            if (c < c1) {
+                if constexpr (u % 4 == 0) load_s(sb[(u / 4 + 1) & 1], c + 4);
+                uint32_t w[RT][4], s[RT][SW];
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                sc[i] = 0;
+                for (int i = 0; i < RT; ++i) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[i].w[j] = 8 * j < valid ? reinterpret_cast<const uint32_t *>(
-                                                    qrow[i] + (k0 >> 1))[j]
-                                              : 0u;
+                    for (int j = 0; j < 4; ++j) w[i][j] = from_lane(from_mk, wb[u % kDepth][i][j]);
 #pragma unroll
-                for (int j = 0; j < 32 / kGroup; ++j)
-                    if (kGroup * j < valid)
-                        sc[i] |= (uint32_t)srow[i][(k0 + kg * 32) / kGroup + j] << (kNV ? 8 * j : 23);
+                    for (int j = 0; j < SW; ++j) s[i][j] = from_lane(from_m + 4 * (u & 3), sb[(u / 4) & 1][i][j]);
+                    if constexpr (kNV) {  // bytes 2 j + kg / 2 to bytes 0 and 2
+#pragma unroll
+                        for (int j = 0; j < SW; ++j) s[i][j] = kg & 2 ? s[i][j] >> 8 : s[i][j];
+                    }
+                    transpose_kg(w[i]);
+                }
+                load_w(wb[u % kDepth], c + kDepth);
+                static_for<0, 4, 1>([&](auto J) {
+                    constexpr int j = J;
+                    bf16x8 b[NT];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const uint4 v = xc[j][t];
+                        b[t] = as_bf16x8(from_lane(from_mk, v.x), from_lane(from_mk, v.y),
+                                         from_lane(from_mk, v.z), from_lane(from_mk, v.w));
+                    }
+                    load_x(j, c + 1);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+                        uint32_t sw;
+                        if constexpr (kNV) sw = s[i][j / 2];
+                        else sw = scale_at<j>(s[i][0]);
+                        const bf16x8 wf = weights8<kNV, 2 * (j & 1)>(w[i][j], sw);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) acc[i][t] = mfma(wf, b[t], acc[i][t]);
+                    }
+                });
             }
-            chunk(w, sc, k0, valid);
+        });
+    }
+    if (chunks * 128 < k && wave == kWaves - 1) {
+        // the last, partial chunk: lane (m, kg) takes k = 32 kg + 8 j .. of it,
+        // as far as it goes, straight from its row
+        const int64_t at = (int64_t)chunks * 128 + kg * 32;
+        const int valid = (int)(k - at);  // 16 (NVFP4) or 32 divides it
+        uint32_t w[RT][4], s[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int64_t r = min(row0 + i * 16 + m, n - 1);
+            s[i] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[i][j] = 8 * j < valid ? reinterpret_cast<const Words<4> *>(a.q + r * (k >> 1) + (at >> 1))->w[j] : 0u;
+#pragma unroll
+            for (int j = 0; j < 32 / kGroup; ++j)
+                if (kGroup * j < valid)
+                    s[i] |= (uint32_t)a.s[r * (k / kGroup) + at / kGroup + j] << (kNV ? 8 * j : 23);
         }
+        static_for<0, 4, 1>([&](auto J) {
+            constexpr int j = J;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const uint16_t *xp = a.x + min(tok0 + t * 16 + m, a.tokens - 1) * a.ldx + at;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (8 * j < valid) v = ld16<false>(xp + 8 * j);
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                    acc[i][t] = mfma(weights8<kNV, j / 2>(w[i][j], s[i]), __builtin_bit_cast(bf16x8, v), acc[i][t]);
+            }
+        });
     }
 
-    __shared__ f32x4 red[kWaves][RT * NT][kWave];
+    // Add the waves' tiles in order.  A tile's 64 lanes are stored with a gap
+    // after every 16, so that neighbouring threads, which take neighbouring
+    // rows of one token, read different banks and write contiguous bytes.
+    constexpr int kTile = 68;
+    __shared__ f32x4 red[kWaves][RT * NT][kTile];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) red[wave][i * NT + t][lane] = acc[i][t];
+        for (int t = 0; t < NT; ++t) red[wave][t * RT + i][lane + kg] = acc[i][t];
     __syncthreads();
-    const float gs = kNV ? *g : 1.0f;
-    for (int e = threadIdx.x; e < RT * NT * kWave; e += kWaves * kWave) {
-        const int tile = e / kWave, l = e % kWave;
-        f32x4 v = red[0][tile][l];
+    for (int e = threadIdx.x; e < RT * NT * 256; e += kWaves * kWave) {
+        const int row = e % (RT * 16), tok = e / (RT * 16);
+        const int tile = (tok >> 4) * RT + (row >> 4), l = (tok & 15) + 17 * ((row >> 2) & 3);
+        float v = red[0][tile][l][row & 3];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) v += red[w][tile][l];
-        const int64_t t = tok0 + (tile % NT) * 16 + (l & 15);
-        const int64_t r = row0 + (tile / NT) * 16 + (l >> 4) * 4;
-        if (t >= tokens) continue;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            if (r + c >= n) break;
-            const float o = kNV ? v[c] * gs : v[c];
-            if (out_f32)
-                static_cast<float *>(y)[t * ldy + r + c] = o;
-            else
-                static_cast<__bf16 *>(y)[t * ldy + r + c] = (__bf16)o;
-        }
+        for (int w = 1; w < kWaves; ++w) v += red[w][tile][l][row & 3];
+        if (tok0 + tok < a.tokens && row0 + row < n)
+            store_y(a.y, (tok0 + tok) * a.ldy + row0 + row, v * gs, a.out_f32);
     }
 }
 
-template <bool kNV, int RT, int NT, int kWaves>
-hipError_t go(const uint16_t *x, int64_t tokens, int64_t ldx, const uint8_t *q, const uint8_t *s,
-              const float *g, int64_t n, int64_t k, void *y, int64_t ldy, bool f32,
-              hipStream_t stream)
+template <bool kNV, int RT, int NT, int kWaves, int kDepth>
+__global__ __launch_bounds__(kWaves * 64) void matvec_many_kernel(MatvecArgs a)
 {
-    const int64_t gx = (n + RT * 16 - 1) / (RT * 16), gy = (tokens + NT * 16 - 1) / (NT * 16);
-    if (gx > 0x7FFFFFFF || gy > 65535) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((fp4_matvec_kernel<kNV, RT, NT, kWaves>), dim3((unsigned)gx, (unsigned)gy),
-                       dim3(kWaves * kWave), 0, stream, x, tokens, ldx, q, s, g, n, k, y, ldy,
-                       (int)f32);
+    many_body<kNV, RT, NT, kWaves, kDepth>(a);
+}
+
+template <bool kNV, int RS, int kWaves, int kDepth>
+hipError_t go_few(const MatvecArgs &a, hipStream_t stream)
+{
+    const int64_t gx = (a.n + RS * 4 - 1) / (RS * 4);
+    if (gx > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((matvec_few_kernel<kNV, RS, kWaves, kDepth>), dim3((unsigned)gx),
+                       dim3(kWaves * kWave), (unsigned)(a.tokens * few_pitch(a.k) * 2), stream, a);
     return hipGetLastError();
 }
 
-template <bool kNV>
-hipError_t pick(const uint16_t *x, int64_t tokens, int64_t ldx, const uint8_t *q, const uint8_t *s,
-                const float *g, int64_t n, int64_t k, void *y, int64_t ldy, bool f32,
-                hipStream_t stream)
+template <bool kNV, int RT, int NT, int kWaves, int kDepth>
+hipError_t go_many(const MatvecArgs &a, hipStream_t stream)
 {
-    if (tokens <= 16) return go<kNV, 1, 1, 8>(x, tokens, ldx, q, s, g, n, k, y, ldy, f32, stream);
-    if (tokens <= 32) return go<kNV, 2, 2, 8>(x, tokens, ldx, q, s, g, n, k, y, ldy, f32, stream);
-    return go<kNV, 2, 4, 8>(x, tokens, ldx, q, s, g, n, k, y, ldy, f32, stream);
+    const int64_t gx = (a.n + RT * 16 - 1) / (RT * 16), gy = (a.tokens + NT * 16 - 1) / (NT * 16);
+    if (gx > 0x7FFFFFFF || gy > 65535) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((matvec_many_kernel<kNV, RT, NT, kWaves, kDepth>),
+                       dim3((unsigned)gx, (unsigned)gy), dim3(kWaves * kWave), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <bool kNV, int RT>
+hipError_t pick_tiles(const MatvecArgs &a, hipStream_t stream)
+{
+    if (a.tokens <= 16) return go_many<kNV, RT, 1, 8, 2>(a, stream);
+    if (a.tokens <= 32) return go_many<kNV, RT, 2, 8, 2>(a, stream);
+    return go_many<kNV, RT, 4, 8, 2>(a, stream);
+}
+
+// Measured on MI355X (us, weights from the memory-side cache), one token x
+// [8192, 8192] MXFP4: 8.7 with 8 rows a workgroup and 8 waves, 10.2 with 16
+// rows and 4 waves; four tokens x [8192, 7168]: 9.5 with 16 rows, 11.3 with 8
+// (each workgroup stages the tokens anew); 16 rows by matvec_many: 11.8.
+//
+// More tokens: every workgroup reads all tokens, so few rows cost L2 traffic,
+// many leave CUs without work.  The least strips that need no more than one
+// workgroup per CU measured best or next to it: 64 tokens x [16384, 7168] 54,
+// 35, 27 with 1, 2, 4 strips; x [4096, 7168] 15.5, 17.3, 22.3; 16 tokens x
+// [8192, 7168] 12.4, 9.7, 11.9; x [2048, 7168] 6.0, 7.2, 10.1.
+template <bool kNV>
+hipError_t pick(const MatvecArgs &a, hipStream_t stream)
+{
+    if (a.tokens <= 4 && a.tokens * few_pitch(a.k) * 2 <= kFewLds)
+        return a.tokens == 1 ? go_few<kNV, 2, 8, 2>(a, stream) : go_few<kNV, 4, 8, 2>(a, stream);
+    constexpr int64_t kCus = 256;
+    if (a.n <= 16 * kCus) return pick_tiles<kNV, 1>(a, stream);
+    if (a.n <= 32 * kCus) return pick_tiles<kNV, 2>(a, stream);
+    return pick_tiles<kNV, 4>(a, stream);
 }
 
 }  // namespace
@@ -229,8 +466,8 @@ hipError_t launch_fp4_matvec(bool nv, const uint16_t *x, int64_t tokens, int64_t
                              const uint8_t *q, const uint8_t *s, const float *g, int64_t n,
                              int64_t k, void *y, int64_t ldy, bool out_f32, hipStream_t stream)
 {
-    return nv ? pick<true>(x, tokens, ldx, q, s, g, n, k, y, ldy, out_f32, stream)
-              : pick<false>(x, tokens, ldx, q, s, g, n, k, y, ldy, out_f32, stream);
+    const MatvecArgs a{x, tokens, ldx, q, s, g, n, k, y, ldy, (int)out_f32};
+    return nv ? pick<true>(a, stream) : pick<false>(a, stream);
 }
 
 }  // namespace mxq

@@ -36,37 +36,13 @@
 // not, a NaN scale is taken out of the product and put into the rows that see
 // it.
 
+#include "fp4_mfma.hpp"
 #include "kv4.hpp"
-#include "mxq_device.hpp"
+
 
 namespace mxq {
 
 namespace {
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-template <int N>
-struct __attribute__((packed, aligned(4))) Words { uint32_t w[N]; };
-
-__device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
-{
-    return __builtin_bit_cast(bf16x8, make_uint4(a, b, c, d));
-}
-
-template <int kByte>
-__device__ __forceinline__ uint32_t fp4_pair(uint32_t codes, uint32_t scale_bits)
-{
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(
-                                            codes, __uint_as_float(scale_bits), kByte));
-}
-
-// Byte i (0..3, constant) of a scale word to the exponent field; other bits junk.
-template <int i>
-__device__ __forceinline__ uint32_t scale_at(uint32_t w)
-{
-    return i == 3 ? w >> 1 : w << (23 - 8 * i);
-}
 
 // Bytes [0, n) of a word.
 __device__ __forceinline__ uint32_t low_bytes(int n)
@@ -213,9 +189,9 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(Kv4Attn a)
                 // dims kg D/4 + 8 j ..: the lane's first or second scale group
                 const uint32_t s = 8 * j + kg * (D / 4) % 32 < 32 ? s0 : s1;
                 const uint32_t w = tl_.kc[u].w[j];
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    as_bf16x8(fp4_pair<0>(w, s), fp4_pair<1>(w, s), fp4_pair<2>(w, s), fp4_pair<3>(w, s)),
-                    qf[j], acc, 0, 0, 0);
+                acc = mfma(
+                    fp4_frag(w, s),
+                    qf[j], acc);
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[4 * u + r] = acc[r] * c;
@@ -302,8 +278,8 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(Kv4Attn a)
                     o[2 * w] = __builtin_amdgcn_perm(t1, t0, 0x07060302u);
                     o[2 * w + 1] = __builtin_amdgcn_perm(t3, t2, 0x07060302u);
                 }
-                oe[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(e[0], e[1], e[2], e[3]), p, oe[g], 0, 0, 0);
-                oo[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(o[0], o[1], o[2], o[3]), p, oo[g], 0, 0, 0);
+                oe[g] = mfma(as_bf16x8(e[0], e[1], e[2], e[3]), p, oe[g]);
+                oo[g] = mfma(as_bf16x8(o[0], o[1], o[2], o[3]), p, oo[g]);
             }
         }
     }

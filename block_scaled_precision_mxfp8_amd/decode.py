@@ -49,49 +49,47 @@ def _rows16(x: torch.Tensor) -> torch.Tensor:
 # ---------------------------------------------------------------------------
 
 def _matvec(fn: str, x, q, s, g, group: int, out_dtype, out):
-    _mxq._need_bf16_cuda(x)
+    if not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 or not x.is_cuda:
+        _mxq._need_bf16_cuda(x)
     dev = x.device
-    if q.dtype != torch.uint8:
+    if q.dtype is not torch.uint8:
         q = q.view(torch.uint8)
-    if s.dtype != torch.uint8:
+    if s.dtype is not torch.uint8:
         s = s.view(torch.uint8)
-    _need(q, "q", torch.uint8, dev)
-    _need(s, "scale", torch.uint8, dev)
-    if q.dim() != 2 or s.dim() != 2:
-        raise ValueError("q and scale must be 2-D")
-    n, k = q.shape[0], 2 * q.shape[1]
-    if x.dim() < 1 or x.shape[-1] != k:
-        raise ValueError(f"x has {x.shape[-1] if x.dim() else 0} columns, the weights {k}")
+    if q.device != dev or s.device != dev:
+        raise ValueError(f"q and scale must be on {dev}")
+    if q.dim() != 2 or not q.is_contiguous() or not s.is_contiguous():
+        raise ValueError("q and scale must be 2-D and contiguous")
+    n, half = q.shape
+    k = 2 * half
+    shape = x.shape
+    if not shape or shape[-1] != k:
+        raise ValueError(f"x has {shape[-1] if shape else 0} columns, the weights {k}")
     if k % group or s.shape != (n, k // group):
         raise ValueError(f"scale must be [{n}, {k}/{group}]")
-    if not q.is_contiguous() or not s.is_contiguous():
-        raise ValueError("q and scale must be contiguous")
-    if out_dtype is torch.bfloat16:
-        f32 = 0
-    elif out_dtype is torch.float32:
-        f32 = 1
-    else:
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError("out_dtype must be bfloat16 or float32")
-    x2 = x if x.dim() == 2 else x.reshape(-1, k)
-    if x2.stride(0) < k:
-        x2 = x2.contiguous()
-    x2 = _rows16(x2)
-    tokens = x2.shape[0]
-    shape = (*x.shape[:-1], n)
+    x2 = x if len(shape) == 2 else x.reshape(-1, k)
+    ldx, unit = x2.stride()
+    xp = x2.data_ptr()
+    if unit != 1 or ldx % 8 or ldx < k or xp % 16:
+        x2 = x2.clone(memory_format=torch.contiguous_format)
+        ldx, xp = k, x2.data_ptr()
+    shape = (*shape[:-1], n)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=dev)
+        out = x.new_empty(shape, dtype=out_dtype)
     else:
         _need(out, "out", out_dtype, dev)
         if tuple(out.shape) != shape or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous {list(shape)} tensor")
-    L = _mxq.load()
-    ldx = x2.stride(0) if tokens > 1 and k else k
+    L = _mxq._lib or _mxq.load()
+    f32 = out_dtype is torch.float32
     if g is None:
-        st = L.mxfp4_matvec(x2.data_ptr(), tokens, ldx, q.data_ptr(), s.data_ptr(), n, k,
+        st = L.mxfp4_matvec(xp, x2.shape[0], ldx, q.data_ptr(), s.data_ptr(), n, k,
                             out.data_ptr(), n, f32, _stream_of(dev))
     else:
-        st = L.nvfp4_matvec(x2.data_ptr(), tokens, ldx, q.data_ptr(), s.data_ptr(), g.data_ptr(),
-                            n, k, out.data_ptr(), n, f32, _stream_of(dev))
+        st = L.nvfp4_matvec(xp, x2.shape[0], ldx, q.data_ptr(), s.data_ptr(), g.data_ptr(), n, k,
+                            out.data_ptr(), n, f32, _stream_of(dev))
     if st:
         raise _mxq.MXQError(fn, st)
     return out

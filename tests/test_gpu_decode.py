@@ -38,7 +38,8 @@ def product(gpu, kind, x, q, s, g, dtype):
 @pytest.mark.parametrize("tokens,n,k", [
     (1, 1, 32), (1, 16, 128), (1, 17, 96), (2, 100, 256), (3, 33, 288), (16, 64, 512), (17, 48, 544),
     (31, 40, 2048), (33, 130, 1056), (64, 64, 4096), (65, 20, 160), (130, 33, 96), (1, 257, 7168), (5, 4097, 320),
-    (1, 3, 2080), (48, 1000, 2336), (1, 40, 16384), (9, 4100, 2080), (64, 2050, 1184),
+    (1, 3, 2080), (48, 1000, 2336), (1, 40, 16384), (9, 4100, 2080), (64, 2050, 1184), (4, 40, 8192), (4, 33, 9376), (3, 70, 544),
+    (20, 8200, 1184), (7, 8195, 672), (40, 8208, 672), (24, 4160, 288),
 ])
 def test_matvec(gpu, kind, tokens, n, k):
     announce(f"matvec {kind} {tokens}x{n}x{k}")
