@@ -72,9 +72,10 @@ hipError_t launch_kv4_copy(uint8_t *cache, int64_t layers, int64_t layer_stride,
                            int64_t page_stride, int64_t page_bytes, const int32_t *src,
                            const int32_t *dst, int64_t n, hipStream_t stream);
 
-// Splits of the context an attention call uses (1 needs no workspace).
+// Splits of the context an attention call uses (1 needs no workspace); never
+// more with a window than without (0).
 int32_t kv4_attention_splits(int64_t seqs, int64_t tokens, int64_t q_heads, int64_t kv_heads,
-                             int64_t dim, int64_t page, int64_t width);
+                             int64_t dim, int64_t page, int64_t width, int64_t window);
 
 hipError_t launch_kv4_attention(const Kv4Attn &a, hipStream_t stream);
 

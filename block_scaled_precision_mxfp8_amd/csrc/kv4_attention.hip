@@ -71,56 +71,181 @@ __device__ __forceinline__ float sum_over_kg(float v)
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// What a lane loads of a tile: K codes of its four tokens, their scales, V
-// codes of 16 tokens x NG dim pairs, their scales.
-template <int D>
-struct Tile {
-    static constexpr int NG = D / 32;
-    static constexpr int kScaleSets = D == 64 || D == 128 ? 1 : 2;  // K scale groups a lane's dims touch
-    Words<NG> kc[4];
-    uint4 ks[kScaleSets];
-    uint4 vc[NG], vs[NG];
-    bool ok;  // the page of the lane's 16 tokens (kg) is in the cache
-};
-
-template <int D>
-__device__ __forceinline__ void load_tile(const Kv4Attn &a, const uint8_t *cache, const int32_t *table,
-                                          int h, int tile, int m, int kg, Tile<D> &t)
+// NG dwords that are read once: 16-byte pieces with the streaming hint where
+// the address allows them (64 sequences of 4096..8192 tokens, 8 heads of 128:
+// 86 us with the hint on K and V codes, 92 without).
+template <int NG>
+__device__ __forceinline__ Words<NG> load_once(const uint8_t *p)
 {
-    constexpr int NG = D / 32;
-    const Kv4Geom &geo = a.geo;
-    const int bpp = geo.page >> 4;  // blocks of 16 tokens in a page
-    auto place = [&](int blk, int &in) {
-        const int p = blk / bpp;
-        in = (blk - p * bpp) * 16;
-        int pg = p < a.width ? table[p] : -1;
-        return pg;
-    };
-    int in;
-    int pg = place(tile * 4 + (m >> 2), in);
-    bool ok = pg >= 0 && pg < geo.pages;
-    {
-        const uint8_t *base = cache + (ok ? pg : 0) * geo.page_stride;
-        const uint8_t *kc = base + geo.k_code(h, in + (m & 3)) + kg * (D / 8);
+    if constexpr (NG % 4 == 0) {
+        uint4 v[NG / 4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) t.kc[u] = *reinterpret_cast<const Words<NG> *>(kc + u * 4 * (D / 2));
-        const int g0 = kg * (D / 4) / 32;
-        const uint8_t *ks = base + geo.k_scales() + geo.scale(h, in, g0);
-        t.ks[0] = ld16<false>(ks);
-        if constexpr (Tile<D>::kScaleSets == 2) t.ks[1] = ld16<false>(ks + (g0 + 1 < NG ? 16 : 0));
+        for (int i = 0; i < NG / 4; ++i) v[i] = ld16<true>(p + 16 * i);
+        return __builtin_bit_cast(Words<NG>, v);
+    } else {
+        return *reinterpret_cast<const Words<NG> *>(p);
     }
-    pg = place(tile * 4 + kg, in);
-    t.ok = pg >= 0 && pg < geo.pages;
+}
+
+constexpr int scale_sets(int dim) { return dim == 64 || dim == 128 ? 1 : 2; }
+
+// The place of a lane's block of 16 tokens: entry of the page table, block in
+// the page, advanced by a constant number of blocks without a division.
+struct Block {
+    int page, in;
+    __device__ __forceinline__ void start(int blk, int per_page)
     {
-        const uint8_t *base = cache + (t.ok ? pg : 0) * geo.page_stride;
-        const uint8_t *vc = base + geo.v_codes() + geo.v_code(h, in, m);
-        const uint8_t *vs = base + geo.v_scales() + geo.scale(h, in, 0);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            t.vc[g] = ld16<false>(vc + g * 256);
-            t.vs[g] = ld16<false>(vs + g * 16);
+        page = blk / per_page;
+        in = blk - page * per_page;
+    }
+    __device__ __forceinline__ void advance(int pages, int blocks, int per_page)
+    {
+        page += pages;
+        in += blocks;
+        if (in >= per_page) {
+            in -= per_page;
+            ++page;
         }
     }
+    // its page, -1 for none
+    __device__ __forceinline__ int look(const int32_t *table, int width) const
+    {
+        return page < width ? table[page] : -1;
+    }
+};
+
+// What a lane loads of K: codes of its four tokens, the scales of their block.
+template <int D>
+struct KTile {
+    static constexpr int NG = D / 32;
+    Words<NG> codes[4];
+    uint4 scales[scale_sets(D)];  // the groups its D / 4 dims touch
+
+    __device__ __forceinline__ void load(const uint8_t *cache, const Kv4Geom &geo, int h, int page, int in, int m, int kg)
+    {
+        const bool ok = page >= 0 && page < geo.pages;
+        const uint8_t *base = cache + (ok ? page : 0) * geo.page_stride;
+        const uint8_t *kc = base + geo.k_code(h, in * 16 + (m & 3)) + kg * (D / 8);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) codes[u] = load_once<NG>(kc + u * 4 * (D / 2));
+        const int g0 = kg * (D / 4) / 32;
+        const uint8_t *ks = base + geo.k_scales() + geo.scale(h, in * 16, g0);
+        scales[0] = ld16<false>(ks);
+        if constexpr (scale_sets(D) == 2) scales[1] = ld16<false>(ks + (g0 + 1 < NG ? 16 : 0));
+    }
+};
+
+// Of V: codes of 16 tokens x NG dim pairs and their scales.
+template <int D>
+struct VTile {
+    static constexpr int NG = D / 32;
+    uint4 codes[NG], scales[NG];
+    bool ok;  // the block's page is in the cache
+
+    __device__ __forceinline__ void load(const uint8_t *cache, const Kv4Geom &geo, int h, int page, int in, int m)
+    {
+        ok = page >= 0 && page < geo.pages;
+        const uint8_t *base = cache + (ok ? page : 0) * geo.page_stride;
+        const uint8_t *vc = base + geo.v_codes() + geo.v_code(h, in * 16, m);
+        const uint8_t *vs = base + geo.v_scales() + geo.scale(h, in * 16, 0);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            codes[g] = ld16<true>(vc + g * 256);
+            scales[g] = ld16<false>(vs + g * 16);
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t word(const uint4 &v, int i)
+{
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// Which tokens rows [row0, row0 + n) of one sequence see: [any_lo, any_hi) by
+// any of them, [all_lo, all_hi) by every one.
+struct Range {
+    int any_lo, any_hi, all_lo, all_hi;
+    __device__ __forceinline__ Range(const Kv4Attn &a, int len, int group, int row0, int n)
+    {
+        const int rows = a.tokens * group;
+        const int first = len - a.tokens + row0 / group, last = len - a.tokens + min(row0 + n - 1, rows - 1) / group;
+        any_lo = a.window > 0 ? max(first - a.window + 1, 0) : 0;
+        any_hi = a.causal ? max(last + 1, 0) : len;
+        all_lo = a.window > 0 ? max(last - a.window + 1, 0) : 0;
+        all_hi = a.causal ? max(first + 1, 0) : len;
+    }
+};
+
+__device__ __forceinline__ int context_length(const Kv4Attn &a, int b)
+{
+    return a.geo.pages > 0 ? min(max(a.lengths[b], 0), a.width * a.geo.page) : 0;
+}
+
+// Scores to base-2 exponents: exp(scale s) = 2^(c s).  A negative scale is
+// carried by q's signs, so that c is positive and the largest score can be
+// found before multiplying; a zero scale becomes one that makes every score 0.
+__device__ __forceinline__ float exponent_factor(float scale)
+{
+    const float c = __builtin_fabsf(scale) * kLog2e;
+    return c == 0.f ? 0x1p-120f : c;
+}
+
+__device__ __forceinline__ bf16x8 load_q(const uint16_t *p, float scale)
+{
+    const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
+    const uint4 v = ld16<false>(p);
+    return as_bf16x8(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+}
+
+// One step of a row's running softmax over the 16 scores of each of its four
+// lanes: x becomes the weights 2^(c x - c max), the running maximum (unscaled)
+// and this lane's sum move on, and the row's earlier sums want the returned
+// factor when `moved`.
+__device__ __forceinline__ float softmax_step(float (&x)[16], float c, float &mx, float &sum, bool &moved)
+{
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
+    const float mx_new = fmaxf(mx, max_over_kg(top));
+    const float base = mx_new == -INFINITY ? 0.f : mx_new * c;
+    float f = 1.f;
+    moved = wave_any(mx_new > mx);
+    if (moved) {
+        f = __builtin_amdgcn_exp2f(mx * c - base);
+        sum *= f;
+        mx = mx_new;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -base));
+        sum += x[i];
+    }
+    return f;
+}
+
+__device__ __forceinline__ bf16x8 weights_frag(const float (&x)[16], int s)
+{
+    return as_bf16x8(bf16x2_rne(x[8 * s], x[8 * s + 1]), bf16x2_rne(x[8 * s + 2], x[8 * s + 3]),
+                     bf16x2_rne(x[8 * s + 4], x[8 * s + 5]), bf16x2_rne(x[8 * s + 6], x[8 * s + 7]));
+}
+
+// V^T operands of 8 tokens (code and scale words of tokens 0..3 and 4..7) for
+// a lane's even and odd dim.
+__device__ __forceinline__ void v_frags(uint32_t c0, uint32_t c1, uint32_t s0, uint32_t s1, bf16x8 &even, bf16x8 &odd)
+{
+    uint32_t e[4], o[4];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const uint32_t c = w ? c1 : c0, s = w ? s1 : s0;
+        const uint32_t t0 = fp4_pair<0>(c, scale_at<0>(s)), t1 = fp4_pair<1>(c, scale_at<1>(s));
+        const uint32_t t2 = fp4_pair<2>(c, scale_at<2>(s)), t3 = fp4_pair<3>(c, scale_at<3>(s));
+        e[2 * w] = __builtin_amdgcn_perm(t1, t0, 0x05040100u);
+        e[2 * w + 1] = __builtin_amdgcn_perm(t3, t2, 0x05040100u);
+        o[2 * w] = __builtin_amdgcn_perm(t1, t0, 0x07060302u);
+        o[2 * w + 1] = __builtin_amdgcn_perm(t3, t2, 0x07060302u);
+    }
+    even = as_bf16x8(e[0], e[1], e[2], e[3]);
+    odd = as_bf16x8(o[0], o[1], o[2], o[3]);
 }
 
 // kWaves waves take the 64-token tiles of one split in turn, each with its own
@@ -136,21 +261,15 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(Kv4Attn a)
     const int h = blockIdx.x % heads, b = blockIdx.x / heads, split = blockIdx.z;
     const int rows = T * group, row0 = blockIdx.y * 16;
 
-    const int cap = a.width * a.geo.page;
-    const int len = a.geo.pages > 0 ? min(max(a.lengths[b], 0), cap) : 0;
+    const int len = context_length(a, b);
     const int row = min(row0 + m, rows - 1);
     const int t = row / group, hq = h * group + (row - t * group);
     // visible tokens of this lane's row: [jlo, jhi)
     const int pos = len - T + t;
     const int jhi = a.causal ? max(pos + 1, 0) : len;
     const int jlo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
-    // of any and of every row of the tile
-    const int tf = row0 / group, tl = min(row0 + 15, rows - 1) / group;
-    const int any_lo = a.window > 0 ? max(len - T + tf - a.window + 1, 0) : 0;
-    const int any_hi = a.causal ? max(len - T + tl + 1, 0) : len;
-    const int all_lo = a.window > 0 ? max(len - T + tl - a.window + 1, 0) : 0;
-    const int all_hi = a.causal ? max(len - T + tf + 1, 0) : len;
-    const int tile0 = any_lo / 64, ntiles = any_hi > any_lo ? (any_hi + 63) / 64 - tile0 : 0;
+    const Range see(a, len, group, row0, 16);
+    const int tile0 = see.any_lo / 64, ntiles = see.any_hi > see.any_lo ? (see.any_hi + 63) / 64 - tile0 : 0;
     const int per = (ntiles + a.splits - 1) / a.splits;
     const int tile_end = tile0 + min(ntiles, (split + 1) * per);
 
@@ -158,10 +277,10 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(Kv4Attn a)
     {
         const uint16_t *qp = a.q + b * a.q_seq + t * a.q_tok + hq * a.q_head + kg * (D / 4);
 #pragma unroll
-        for (int j = 0; j < NG; ++j) qf[j] = __builtin_bit_cast(bf16x8, ld16<false>(qp + 8 * j));
+        for (int j = 0; j < NG; ++j) qf[j] = load_q(qp + 8 * j, a.scale);
     }
     const int32_t *table = a.table + b * a.table_stride;
-    const float c = a.scale * kLog2e;
+    const float c = exponent_factor(a.scale);
     const int rot = (8 * (m & 3) + 9) & 31;  // scale byte m % 4 of a word -> bits 23..30
 
     f32x4 oe[NG], oo[NG];  // even and odd dims
@@ -169,48 +288,66 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(Kv4Attn a)
     for (int g = 0; g < NG; ++g) oe[g] = oo[g] = f32x4{0.f, 0.f, 0.f, 0.f};
     float mx = -INFINITY, sum = 0.f;
 
-    for (int tile = tile0 + split * per + wave; tile < tile_end; tile += kWaves) {
-        Tile<D> tl_;
-        load_tile<D>(a, a.cache, table, h, tile, m, kg, tl_);
-
+    const int bpp = a.geo.page >> 4;  // blocks in a page
+    const int step_pages = 4 * kWaves / bpp, step_blocks = 4 * kWaves - step_pages * bpp;
+    int tile = tile0 + split * per + wave;
+    Block kb, vb;
+    KTile<D> kt;
+    VTile<D> vt;
+    int k_page = -1, v_page = -1;  // of the next tile
+    if (tile < tile_end) {
+        kb.start(tile * 4 + (m >> 2), bpp);
+        vb.start(tile * 4 + kg, bpp);
+        k_page = kb.look(table, a.width);
+        v_page = vb.look(table, a.width);
+        kt.load(a.cache, a.geo, h, k_page, kb.in, m, kg);
+        vt.load(a.cache, a.geo, h, v_page, vb.in, m);
+        kb.advance(step_pages, step_blocks, bpp);
+        vb.advance(step_pages, step_blocks, bpp);
+        k_page = kb.look(table, a.width);
+        v_page = vb.look(table, a.width);
+    }
+    // Each operand's registers are loaded anew as soon as they are used: K of
+    // the next tile is in flight during the softmax and the second product, V
+    // during the first product, page numbers one tile longer.
+    for (; tile < tile_end; tile += kWaves) {
+        const bool more = tile + kWaves < tile_end;
         float x[16];  // tokens 16 kg + 0..15 of the tile
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const uint32_t w0 = u == 0 ? tl_.ks[0].x : u == 1 ? tl_.ks[0].y : u == 2 ? tl_.ks[0].z : tl_.ks[0].w;
-            const uint32_t s0 = __builtin_amdgcn_alignbit(w0, w0, rot);
+            const uint32_t w0 = word(kt.scales[0], u), s0 = __builtin_amdgcn_alignbit(w0, w0, rot);
             uint32_t s1 = s0;
-            if constexpr (Tile<D>::kScaleSets == 2) {
-                const uint32_t w1 = u == 0 ? tl_.ks[1].x : u == 1 ? tl_.ks[1].y : u == 2 ? tl_.ks[1].z : tl_.ks[1].w;
+            if constexpr (scale_sets(D) == 2) {
+                const uint32_t w1 = word(kt.scales[1], u);
                 s1 = __builtin_amdgcn_alignbit(w1, w1, rot);
             }
             f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                // dims kg D/4 + 8 j ..: the lane's first or second scale group
-                const uint32_t s = 8 * j + kg * (D / 4) % 32 < 32 ? s0 : s1;
-                const uint32_t w = tl_.kc[u].w[j];
-                acc = mfma(
-                    fp4_frag(w, s),
-                    qf[j], acc);
-            }
+            for (int j = 0; j < NG; ++j)  // dims kg D/4 + 8 j ..: the lane's first or second scale group
+                acc = mfma(fp4_frag(kt.codes[u].w[j], 8 * j + kg * (D / 4) % 32 < 32 ? s0 : s1), qf[j], acc);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x[4 * u + r] = acc[r] * c;
+            for (int r = 0; r < 4; ++r) x[4 * u + r] = acc[r];
+        }
+        if (more) {
+            kt.load(a.cache, a.geo, h, k_page, kb.in, m, kg);
+            kb.advance(step_pages, step_blocks, bpp);
+            k_page = kb.look(table, a.width);
         }
 
         const int first = tile * 64 + 16 * kg;  // the lane's first token
-        if (tile * 64 < all_lo || tile * 64 + 64 > all_hi || wave_any(!tl_.ok)) {
-            const int lo = tl_.ok ? jlo - first : 16, hi = jhi - first;
+        if (tile * 64 < see.all_lo || tile * 64 + 64 > see.all_hi || wave_any(!vt.ok)) {
+            const int lo = vt.ok ? jlo - first : 16, hi = jhi - first;
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = i >= lo && i < hi ? x[i] : -INFINITY;
             // V scales of tokens no row sees
-            const int alo = tl_.ok ? any_lo - first : 16, ahi = any_hi - first;
+            const int alo = vt.ok ? see.any_lo - first : 16, ahi = see.any_hi - first;
             uint32_t bad = 0;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const uint32_t keep = low_bytes(ahi - 4 * w) & ~low_bytes(alo - 4 * w);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    uint32_t &v = w == 0 ? tl_.vs[g].x : w == 1 ? tl_.vs[g].y : w == 2 ? tl_.vs[g].z : tl_.vs[g].w;
+                    uint32_t &v = w == 0 ? vt.scales[g].x : w == 1 ? vt.scales[g].y : w == 2 ? vt.scales[g].z : vt.scales[g].w;
                     v &= keep;
                     bad |= has_ff(v);
                 }
@@ -221,7 +358,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(Kv4Attn a)
                     bool hit = false;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        uint32_t &v = i / 4 == 0 ? tl_.vs[g].x : i / 4 == 1 ? tl_.vs[g].y : i / 4 == 2 ? tl_.vs[g].z : tl_.vs[g].w;
+                        uint32_t &v = i / 4 == 0 ? vt.scales[g].x : i / 4 == 1 ? vt.scales[g].y : i / 4 == 2 ? vt.scales[g].z : vt.scales[g].w;
                         const uint32_t byte = 0xFFu << (8 * (i & 3));
                         if ((v & byte) == byte) {
                             v &= ~byte;
@@ -240,47 +377,31 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(Kv4Attn a)
             }
         }
 
-        float top = x[0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
-        const float mx_new = fmaxf(mx, max_over_kg(top));
-        const float base = mx_new == -INFINITY ? 0.f : mx_new;
-        if (wave_any(mx_new > mx)) {
-            const float f = __builtin_amdgcn_exp2f(mx - base);
-            sum *= f;
+        bool moved;
+        const float f = softmax_step(x, c, mx, sum, moved);
+        if (moved) {
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 oe[g] *= f;
                 oo[g] *= f;
             }
-            mx = mx_new;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            x[i] = __builtin_amdgcn_exp2f(x[i] - base);
-            sum += x[i];
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const bf16x8 p = as_bf16x8(bf16x2_rne(x[8 * s], x[8 * s + 1]), bf16x2_rne(x[8 * s + 2], x[8 * s + 3]),
-                                       bf16x2_rne(x[8 * s + 4], x[8 * s + 5]), bf16x2_rne(x[8 * s + 6], x[8 * s + 7]));
+            const bf16x8 p = weights_frag(x, s);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                uint32_t e[4], o[4];
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const uint32_t codes = s == 0 ? (w == 0 ? tl_.vc[g].x : tl_.vc[g].y) : (w == 0 ? tl_.vc[g].z : tl_.vc[g].w);
-                    const uint32_t sc = s == 0 ? (w == 0 ? tl_.vs[g].x : tl_.vs[g].y) : (w == 0 ? tl_.vs[g].z : tl_.vs[g].w);
-                    const uint32_t t0 = fp4_pair<0>(codes, scale_at<0>(sc)), t1 = fp4_pair<1>(codes, scale_at<1>(sc));
-                    const uint32_t t2 = fp4_pair<2>(codes, scale_at<2>(sc)), t3 = fp4_pair<3>(codes, scale_at<3>(sc));
-                    e[2 * w] = __builtin_amdgcn_perm(t1, t0, 0x05040100u);
-                    e[2 * w + 1] = __builtin_amdgcn_perm(t3, t2, 0x05040100u);
-                    o[2 * w] = __builtin_amdgcn_perm(t1, t0, 0x07060302u);
-                    o[2 * w + 1] = __builtin_amdgcn_perm(t3, t2, 0x07060302u);
-                }
-                oe[g] = mfma(as_bf16x8(e[0], e[1], e[2], e[3]), p, oe[g]);
-                oo[g] = mfma(as_bf16x8(o[0], o[1], o[2], o[3]), p, oo[g]);
+                bf16x8 e, o;
+                v_frags(word(vt.codes[g], 2 * s), word(vt.codes[g], 2 * s + 1), word(vt.scales[g], 2 * s),
+                        word(vt.scales[g], 2 * s + 1), e, o);
+                oe[g] = mfma(e, p, oe[g]);
+                oo[g] = mfma(o, p, oo[g]);
             }
+        }
+        if (more) {
+            vt.load(a.cache, a.geo, h, v_page, vb.in, m);
+            vb.advance(step_pages, step_blocks, bpp);
+            v_page = vb.look(table, a.width);
         }
     }
 
@@ -290,7 +411,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(Kv4Attn a)
     __shared__ float sm[kWaves][16], sl[kWaves][16];
     sum = sum_over_kg(sum);
     if (kg == 0) {
-        sm[wave][m] = mx;
+        sm[wave][m] = mx * c;
         sl[wave][m] = sum;
     }
 #pragma unroll
@@ -339,62 +460,383 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(Kv4Attn a)
     if (a.lse && d0 == 0) a.lse[line] = (top + __builtin_log2f(total)) * kLn2;
 }
 
-// Joins the splits of one row per workgroup of D / 2 threads.
-__global__ __launch_bounds__(128) void kv4_join_kernel(const float *__restrict__ part, int64_t lines,
-                                                       int splits, int dim, uint16_t *__restrict__ out,
-                                                       float *__restrict__ lse)
+// ---------------------------------------------------------------------------
+// Many rows: eight waves of MT x 16 rows each share the tiles.  A tile's K and V
+// are decoded once, an eighth by each wave, into LDS as whole matrix operands
+// (1 KiB each, lane by lane, so that reads and writes are free of conflicts),
+// two tiles deep: while one is multiplied the next is decoded and the one
+// after it is on its way from memory.  One barrier a tile.
+// ---------------------------------------------------------------------------
+constexpr int kShareWaves = 8;
+
+template <int D, int MT>
+__global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv4Attn a)
 {
-    const int64_t line = blockIdx.x;
-    const float *ml = part + splits * lines * dim;
-    float top = -INFINITY;
-    for (int s = 0; s < splits; ++s) top = fmaxf(top, ml[(s * lines + line) * 2]);
-    const float base = top == -INFINITY ? 0.f : top;
-    float total = 0.f, o0 = 0.f, o1 = 0.f;
-    for (int s = 0; s < splits; ++s) {
-        const float f = __builtin_amdgcn_exp2f(ml[(s * lines + line) * 2] - base);
-        total += ml[(s * lines + line) * 2 + 1] * f;
-        const float2 v = reinterpret_cast<const float2 *>(part + (s * lines + line) * dim)[threadIdx.x];
-        o0 += v.x * f;
-        o1 += v.y * f;
+    constexpr int NG = D / 32, kHalf = (NG + 1) / 2;
+    constexpr int kVRounds = (2 * NG + kShareWaves - 1) / kShareWaves;
+    extern __shared__ __align__(16) uint4 shared_frags[];
+    uint4 *const kf = shared_frags, *const vf = kf + 2 * 4 * NG * kWave;  // [buffer][frag][lane]
+    __shared__ uint32_t nan_tokens[2][NG][8];  // of a masked tile: bit i of [g][2 kg + s]: token 16 kg + 8 s + i
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int m = lane & 15, kg = lane >> 4;
+    const int heads = a.geo.heads, group = a.q_heads / heads, T = a.tokens;
+    const int h = blockIdx.x % heads, b = blockIdx.x / heads, split = blockIdx.z;
+    const int rows = T * group, block0 = blockIdx.y * (kShareWaves * MT * 16), row0 = block0 + wave * (MT * 16);
+
+    const int len = context_length(a, b);
+    const Range see(a, len, group, block0, kShareWaves * MT * 16);
+    const int tile0 = see.any_lo / 64, ntiles = see.any_hi > see.any_lo ? (see.any_hi + 63) / 64 - tile0 : 0;
+    const int per = (ntiles + a.splits - 1) / a.splits;
+    const int begin = tile0 + split * per, end = tile0 + min(ntiles, (split + 1) * per);
+
+    bf16x8 qf[MT][NG];
+    int jlo[MT], jhi[MT];
+    int64_t line[MT];
+    const float c = exponent_factor(a.scale);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int row = min(row0 + 16 * i + m, rows - 1), t = row / group, hq = h * group + (row - t * group);
+        const int pos = len - T + t;
+        jhi[i] = a.causal ? max(pos + 1, 0) : len;
+        jlo[i] = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+        line[i] = ((int64_t)b * T + t) * a.q_heads + hq;
+        const uint16_t *qp = a.q + b * a.q_seq + t * a.q_tok + hq * a.q_head + kg * (D / 4);
+#pragma unroll
+        for (int j = 0; j < NG; ++j) qf[i][j] = load_q(qp + 8 * j, a.scale);
     }
-    const float inv = total == 0.f ? 0.f : 1.0f / total;
-    reinterpret_cast<uint32_t *>(out + line * dim)[threadIdx.x] =
-        (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)(o0 * inv)) |
-        (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)(o1 * inv)) << 16;
-    if (lse && threadIdx.x == 0) lse[line] = (top + __builtin_log2f(total)) * kLn2;
+    f32x4 oe[MT][NG], oo[MT][NG];  // even and odd dims
+    float mx[MT], sum[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        mx[i] = -INFINITY;
+        sum[i] = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) oe[i][g] = oo[i][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // This wave's share of a tile: K of tokens u = wave / 2, half the dwords;
+    // V of (g, s) = (unit / 2, unit % 2), unit = wave + 8 r.
+    const int32_t *table = a.table + b * a.table_stride;
+    const int bpp = a.geo.page >> 4, step_pages = 4 / bpp, step_blocks = 4 - step_pages * bpp;
+    const int ku = wave >> 1, kj = (wave & 1) * kHalf, kn = wave & 1 ? NG - kHalf : kHalf;
+    const int rot = (8 * (m & 3) + 9) & 31;
+    Block kb, vb;
+    int k_page = -1, v_page = -1;
+    uint32_t kc[kHalf], ks[scale_sets(D)];
+    uint2 vc[kVRounds], vs[kVRounds];
+    bool v_ok = false;
+    auto load = [&]() {  // the tile the blocks stand at; then on to the next
+        {
+            const bool ok = k_page >= 0 && k_page < a.geo.pages;
+            const uint8_t *base = a.cache + (ok ? k_page : 0) * a.geo.page_stride;
+            const uint8_t *p = base + a.geo.k_code(h, kb.in * 16 + 4 * ku + (m & 3)) + kg * (D / 8) + 4 * kj;
+            if (NG % 2 == 0 || kn == kHalf) {
+                const Words<kHalf> v = *reinterpret_cast<const Words<kHalf> *>(p);
+#pragma unroll
+                for (int j = 0; j < kHalf; ++j) kc[j] = v.w[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < kHalf; ++j) kc[j] = j < kn ? reinterpret_cast<const uint32_t *>(p)[j] : 0u;
+            }
+            // the group of this wave's first dim of the lane, and the one after it
+            const int g0 = D == 256 ? 2 * kg + (wave & 1) : kg * (D / 4) / 32;
+            const uint8_t *sp = base + a.geo.k_scales() + a.geo.scale(h, kb.in * 16, g0) + 4 * ku;
+            ks[0] = ld4<false>(sp);
+            if constexpr (scale_sets(D) == 2) ks[1] = D == 256 ? ks[0] : ld4<false>(sp + (g0 + 1 < NG ? 16 : 0));
+        }
+        v_ok = v_page >= 0 && v_page < a.geo.pages;
+        const uint8_t *base = a.cache + (v_ok ? v_page : 0) * a.geo.page_stride;
+#pragma unroll
+        for (int r = 0; r < kVRounds; ++r) {
+            const int unit = wave + kShareWaves * r, g = unit >> 1, s = unit & 1;
+            if (unit < 2 * NG) {
+                vc[r] = ld8<false>(base + a.geo.v_codes() + a.geo.v_code(h, vb.in * 16, 16 * g + m) + 8 * s);
+                vs[r] = ld8<false>(base + a.geo.v_scales() + a.geo.scale(h, vb.in * 16, g) + 8 * s);
+            }
+        }
+        kb.advance(step_pages, step_blocks, bpp);
+        vb.advance(step_pages, step_blocks, bpp);
+        k_page = kb.look(table, a.width);
+        v_page = vb.look(table, a.width);
+    };
+    auto masked = [&](int tile, bool ok) {
+        return tile * 64 < see.all_lo || tile * 64 + 64 > see.all_hi || wave_any(!ok);
+    };
+    auto decode = [&](int tile, int buf) {
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) {
+            if (j < kn) {
+                uint32_t w = ks[0];
+                if constexpr (scale_sets(D) == 2)
+                    w = D == 256 || 8 * (kj + j) + kg * (D / 4) % 32 < 32 ? ks[0] : ks[1];
+                const bf16x8 f = fp4_frag(kc[j], __builtin_amdgcn_alignbit(w, w, rot));
+                kf[((buf * 4 + ku) * NG + kj + j) * kWave + lane] = __builtin_bit_cast(uint4, f);
+            }
+        }
+        const bool mask = masked(tile, v_ok);
+#pragma unroll
+        for (int r = 0; r < kVRounds; ++r) {
+            const int unit = wave + kShareWaves * r, g = unit >> 1, s = unit & 1;
+            if (unit < 2 * NG) {
+                if (mask) {  // scales of tokens no row sees, and NaN scales, leave the product
+                    const int first = tile * 64 + 16 * kg + 8 * s;
+                    const int lo = v_ok ? see.any_lo - first : 8, hi = see.any_hi - first;
+                    vs[r].x &= low_bytes(hi) & ~low_bytes(lo);
+                    vs[r].y &= low_bytes(hi - 4) & ~low_bytes(lo - 4);
+                    uint32_t nan = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t &w = i < 4 ? vs[r].x : vs[r].y;
+                        const uint32_t byte = 0xFFu << (8 * (i & 3));
+                        if ((w & byte) == byte) {
+                            w &= ~byte;
+                            nan |= 1u << i;
+                        }
+                    }
+                    if (m == 0) nan_tokens[buf][g][2 * kg + s] = nan;
+                }
+                bf16x8 e, o;
+                v_frags(vc[r].x, vc[r].y, vs[r].x, vs[r].y, e, o);
+                uint4 *p = vf + ((buf * 2 * NG + unit) * 2) * kWave + lane;
+                p[0] = __builtin_bit_cast(uint4, e);
+                p[kWave] = __builtin_bit_cast(uint4, o);
+            }
+        }
+    };
+
+    bool ok = true, ok_next = true;  // of this lane's block of the tile multiplied, and of the next
+    if (begin < end) {
+        kb.start(begin * 4 + (m >> 2), bpp);
+        vb.start(begin * 4 + kg, bpp);
+        k_page = kb.look(table, a.width);
+        v_page = vb.look(table, a.width);
+        load();
+        ok_next = v_ok;
+        decode(begin, 0);
+        if (begin + 1 < end) load();
+    }
+    __syncthreads();
+    const bool work = row0 < rows;  // a wave without rows only decodes
+    for (int tile = begin; tile < end; ++tile) {
+        const int buf = (tile - begin) & 1;
+        ok = ok_next;
+        if (tile + 1 < end) {
+            ok_next = v_ok;
+            decode(tile + 1, buf ^ 1);
+            if (tile + 2 < end) load();
+        }
+        if (work) {
+            float x[MT][16];  // tokens 16 kg + 0..15 of the tile
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                f32x4 acc[MT];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    const bf16x8 f = __builtin_bit_cast(bf16x8, kf[((buf * 4 + u) * NG + j) * kWave + lane]);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) acc[i] = mfma(f, qf[i][j], acc[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) x[i][4 * u + r] = acc[i][r];
+            }
+            if (masked(tile, ok)) {
+                const int first = tile * 64 + 16 * kg;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const int lo = ok ? jlo[i] - first : 16, hi = jhi[i] - first;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[i][e] = e >= lo && e < hi ? x[i][e] : -INFINITY;
+                    // tokens this row sees, as bits; those with a NaN scale spoil the group
+                    const uint32_t seen = lo < 16 && hi > 0 ? ((1u << min(hi, 16)) - 1u) & ~((1u << max(lo, 0)) - 1u) : 0u;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const uint32_t nan = nan_tokens[buf][g][2 * kg] | nan_tokens[buf][g][2 * kg + 1] << 8;
+                        if (!wave_any(nan != 0)) continue;
+                        int any = (nan & seen) != 0;
+                        any |= __shfl_xor(any, 16, kWave);
+                        any |= __shfl_xor(any, 32, kWave);
+                        if (any) {
+                            oe[i][g] += f32x4{NAN, NAN, NAN, NAN};
+                            oo[i][g] += f32x4{NAN, NAN, NAN, NAN};
+                        }
+                    }
+                }
+            }
+            bf16x8 p[MT][2];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                bool moved;
+                const float f = softmax_step(x[i], c, mx[i], sum[i], moved);
+                if (moved) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        oe[i][g] *= f;
+                        oo[i][g] *= f;
+                    }
+                }
+                p[i][0] = weights_frag(x[i], 0);
+                p[i][1] = weights_frag(x[i], 1);
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const uint4 *f = vf + ((buf * 2 * NG + 2 * g + s) * 2) * kWave + lane;
+                    const bf16x8 e = __builtin_bit_cast(bf16x8, f[0]), o = __builtin_bit_cast(bf16x8, f[kWave]);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        oe[i][g] = mfma(e, p[i][s], oe[i][g]);
+                        oo[i][g] = mfma(o, p[i][s], oo[i][g]);
+                    }
+                }
+        }
+        __syncthreads();
+    }
+
+    // lane (m, kg) holds dims 32 g + 8 kg + 0..7 of row m
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        if (row0 + 16 * i + m >= rows) continue;
+        const float total = sum_over_kg(sum[i]), top = mx[i] * c;
+        if (a.splits > 1) {
+            const int64_t lines = (int64_t)a.seqs * T * a.q_heads;
+            float *part = a.part + (split * lines + line[i]) * D + 8 * kg;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                *reinterpret_cast<f32x4 *>(part + 32 * g) = f32x4{oe[i][g][0], oo[i][g][0], oe[i][g][1], oo[i][g][1]};
+                *reinterpret_cast<f32x4 *>(part + 32 * g + 4) = f32x4{oe[i][g][2], oo[i][g][2], oe[i][g][3], oo[i][g][3]};
+            }
+            if (kg == 0) {
+                float *ml = a.part + a.splits * lines * D + (split * lines + line[i]) * 2;
+                ml[0] = top;
+                ml[1] = total;
+            }
+        } else {
+            const float inv = total == 0.f ? 0.f : 1.0f / total;
+            uint16_t *out = a.out + line[i] * D + 8 * kg;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const bf16x8 v = {(__bf16)(oe[i][g][0] * inv), (__bf16)(oo[i][g][0] * inv), (__bf16)(oe[i][g][1] * inv),
+                                  (__bf16)(oo[i][g][1] * inv), (__bf16)(oe[i][g][2] * inv), (__bf16)(oo[i][g][2] * inv),
+                                  (__bf16)(oe[i][g][3] * inv), (__bf16)(oo[i][g][3] * inv)};
+                *reinterpret_cast<bf16x8 *>(out + 32 * g) = v;
+            }
+            if (a.lse && kg == 0) a.lse[line[i]] = (top + __builtin_log2f(total)) * kLn2;
+        }
+    }
 }
 
-constexpr int kWavesPerGroup = 4;
+constexpr int kMaxSplits = 128;
+
+// Joins the splits of one row per workgroup: 256 / (D / 4) of them at a time,
+// four dims a thread, then those groups through LDS.
+template <int D>
+__global__ __launch_bounds__(256) void kv4_join_kernel(const float *__restrict__ part, int64_t lines,
+                                                       int splits, uint16_t *__restrict__ out,
+                                                       float *__restrict__ lse)
+{
+    constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
+    const int64_t line = blockIdx.x;
+    __shared__ float sm[kMaxSplits], sl[kMaxSplits];
+    __shared__ f32x4 so[kGroups][kLanes];
+    const int t = threadIdx.x, d = t % kLanes, group = t / kLanes;
+    if (t < splits) {
+        const float2 v = reinterpret_cast<const float2 *>(part + splits * lines * D)[t * lines + line];
+        sm[t] = v.x;
+        sl[t] = v.y;
+    }
+    __syncthreads();
+    float top = -INFINITY;
+    for (int s = 0; s < splits; ++s) top = fmaxf(top, sm[s]);
+    const float base = top == -INFINITY ? 0.f : top;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    if (group < kGroups) {
+#pragma unroll 4
+        for (int s = group; s < splits; s += kGroups) {
+            const f32x4 v = reinterpret_cast<const f32x4 *>(part + (s * lines + line) * D)[d];
+            o += v * __builtin_amdgcn_exp2f(sm[s] - base);
+        }
+        so[group][d] = o;
+    }
+    __syncthreads();
+    if (t >= kLanes) return;
+    float total = 0.f;
+    for (int s = 0; s < splits; ++s) total += sl[s] * __builtin_amdgcn_exp2f(sm[s] - base);
+    o = so[0][t];
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) o += so[i][t];
+    o *= total == 0.f ? 0.f : 1.0f / total;
+    const uint2 packed = make_uint2(
+        (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)o[0]) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)o[1]) << 16,
+        (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)o[2]) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)o[3]) << 16);
+    reinterpret_cast<uint2 *>(out + line * D)[t] = packed;
+    if (lse && t == 0) lse[line] = (top + __builtin_log2f(total)) * kLn2;
+}
+
+// Waves of a workgroup.  Eight as long as their registers fit (256 each).
+constexpr int waves_for(int dim) { return dim <= 128 ? 8 : 4; }
+
+// Row tiles of a wave of the many-row kernel.
+constexpr int row_tiles(int dim, int64_t rows) { return dim <= 128 && rows > 128 ? 2 : 1; }
+
+// Rows (query tokens x query heads of one kv head) from which K and V are
+// decoded once for all.
+constexpr int64_t kManyRows = 33;
+
+template <int D, int MT>
+hipError_t go_rows(const Kv4Attn &a, int64_t rows, hipStream_t stream)
+{
+    const int64_t gx = (int64_t)a.seqs * a.geo.heads, gy = (rows + kShareWaves * MT * 16 - 1) / (kShareWaves * MT * 16);
+    if (gx > 0x7FFFFFFF || gy > 65535) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((kv4_attention_rows_kernel<D, MT>), dim3((unsigned)gx, (unsigned)gy, (unsigned)a.splits),
+                       dim3(kShareWaves * kWave), 2 * 8 * (D / 32) * kWave * sizeof(uint4), stream, a);
+    return hipGetLastError();
+}
 
 template <int D>
 hipError_t go(const Kv4Attn &a, hipStream_t stream)
 {
-    const int64_t mt = ((int64_t)a.tokens * (a.q_heads / a.geo.heads) + 15) / 16;
-    const int64_t gx = (int64_t)a.seqs * a.geo.heads;
-    if (gx > 0x7FFFFFFF || mt > 65535) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((kv4_attention_kernel<D, kWavesPerGroup>),
-                       dim3((unsigned)gx, (unsigned)mt, (unsigned)a.splits), dim3(kWavesPerGroup * kWave),
-                       0, stream, a);
-    hipError_t e = hipGetLastError();
+    constexpr int kWaves = waves_for(D);
+    const int64_t rows = (int64_t)a.tokens * (a.q_heads / a.geo.heads);
+    const int64_t gx = (int64_t)a.seqs * a.geo.heads, lines = (int64_t)a.seqs * a.tokens * a.q_heads;
+    if (gx > 0x7FFFFFFF || lines > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    hipError_t e;
+    if (rows >= kManyRows) {
+        e = row_tiles(D, rows) == 2 ? go_rows<D, D <= 128 ? 2 : 1>(a, rows, stream) : go_rows<D, 1>(a, rows, stream);
+    } else {
+        hipLaunchKernelGGL((kv4_attention_kernel<D, kWaves>), dim3((unsigned)gx, (unsigned)((rows + 15) / 16), (unsigned)a.splits),
+                           dim3(kWaves * kWave), 0, stream, a);
+        e = hipGetLastError();
+    }
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t lines = (int64_t)a.seqs * a.tokens * a.q_heads;
-    if (lines > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(kv4_join_kernel, dim3((unsigned)lines), dim3(D / 2), 0, stream, a.part, lines,
-                       a.splits, D, a.out, a.lse);
+    hipLaunchKernelGGL((kv4_join_kernel<D>), dim3((unsigned)lines), dim3(256), 0, stream, a.part, lines,
+                       a.splits, a.out, a.lse);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// Splitting the context fills the CUs when there are few rows, but costs a
+// second launch and the partial sums; a wave (with few rows) should have two
+// tiles at least, a workgroup with many rows eight.
 int32_t kv4_attention_splits(int64_t seqs, int64_t tokens, int64_t q_heads, int64_t kv_heads,
-                             int64_t dim, int64_t page, int64_t width)
+                             int64_t dim, int64_t page, int64_t width, int64_t window)
 {
-    (void)dim;
-    const int64_t groups = (tokens * (q_heads / kv_heads) + 15) / 16 * seqs * kv_heads;
-    const int64_t tiles = (width * page + 63) / 64;
-    const int64_t fill = (1024 + groups - 1) / groups;  // 4 workgroups per CU
-    int64_t s = fill < tiles / kWavesPerGroup ? fill : tiles / kWavesPerGroup;
-    return (int32_t)(s < 1 ? 1 : s > 128 ? 128 : s);
+    const int64_t rows = tokens * (q_heads / kv_heads);
+    const bool many = rows >= kManyRows;
+    const int64_t tile = many ? kShareWaves * row_tiles((int)dim, rows) * 16 : 16;
+    const int64_t groups = (rows + tile - 1) / tile * seqs * kv_heads;
+    int64_t seen = width * page;
+    if (window > 0 && window + tokens + 64 < seen) seen = window + tokens + 64;
+    const int64_t fill = (256 + groups - 1) / groups;  // a workgroup per CU
+    const int64_t most = (seen + 63) / 64 / (many ? 8 : 2 * waves_for((int)dim));
+    const int64_t s = fill < most ? fill : most;
+    return (int32_t)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
 }
 
 hipError_t launch_kv4_attention(const Kv4Attn &a, hipStream_t stream)

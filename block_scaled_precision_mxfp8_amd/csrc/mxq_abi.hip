@@ -740,7 +740,7 @@ size_t mxfp4_kv_attention_workspace_size(int32_t seqs, int32_t tokens, int32_t q
         !kv_shape_ok(kv_heads, head_dim, page_size) || q_heads % kv_heads)
         return 0;
     const int32_t splits =
-        mxq::kv4_attention_splits(seqs, tokens, q_heads, kv_heads, head_dim, page_size, width);
+        mxq::kv4_attention_splits(seqs, tokens, q_heads, kv_heads, head_dim, page_size, width, 0);
     if (splits <= 1) return 0;
     return (size_t)splits * seqs * tokens * q_heads * (head_dim + 2) * sizeof(float);
 }
@@ -795,7 +795,7 @@ mxq_status mxfp4_kv_attention(const mxq_kv_cache *cache, const mxq_kv_attention 
     a.lse = args->lse;
     a.part = static_cast<float *>(args->workspace);
     a.splits = need > 0 ? mxq::kv4_attention_splits(a.seqs, a.tokens, a.q_heads, a.geo.heads,
-                                                    a.geo.dim, a.geo.page, a.width)
+                                                    a.geo.dim, a.geo.page, a.width, a.window)
                         : 1;
     return from_hip(mxq::launch_kv4_attention(a, as_stream(stream)));
 }

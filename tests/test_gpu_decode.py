@@ -237,13 +237,15 @@ def attend(gpu, geo, cache, host, q, table, lengths, scale=None, causal=True, wi
 
 
 @pytest.mark.parametrize("geo", GEOS, ids=str)
-@pytest.mark.parametrize("tokens,group", [(1, 1), (1, 8), (2, 5), (4, 4), (7, 3), (33, 2)])
+@pytest.mark.parametrize("tokens,group", [(1, 1), (1, 8), (2, 5), (4, 4), (7, 3), (33, 2), (70, 4)])
 def test_attention(gpu, geo, tokens, group):
     """Ragged lengths from none to many tiles, every mask."""
     heads, dim, page = geo
     announce(f"attention {geo} tokens {tokens} group {group}")
     rng = np.random.default_rng(dim * 100 + tokens)
     lengths = np.array([0, 1, tokens - 1, tokens, 15, 16, 17, 63, 64, 65, 333, 700], np.int32)
+    if tokens > 64:  # the plain form takes long
+        lengths = lengths[[0, 2, 9, 11]]
     width = -(-700 // page)
     cache, host = filled_cache(rng, geo, 40)
     table = rng.integers(0, 40, (len(lengths), width), dtype=np.int32)
