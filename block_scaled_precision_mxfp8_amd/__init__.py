@@ -92,7 +92,7 @@ SIGNATURES = {
     "nvfp4_matvec": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, ctypes.c_int, _vp]),
     "mxfp4_kv_page_bytes": (_sz, [_i32, _i32, _i32]),
     "mxfp4_kv_append": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
-    "mxfp4_kv_attention_workspace_size": (_sz, [_i32] * 7),
+    "mxfp4_kv_attention_workspace_size": (_sz, [_i32] * 8),
     "mxfp4_kv_attention": (ctypes.c_int, [_vp, _vp, _vp]),
     "mxfp4_kv_copy_pages": (ctypes.c_int, [_vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp]),
 }

@@ -628,14 +628,24 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
         }
         if (work) {
             float x[MT][16];  // tokens 16 kg + 0..15 of the tile
+            uint4 kk[2][NG], vv[2][4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
+                if (u == 0) {
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) kk[0][j] = kf[((buf * 4) * NG + j) * kWave + lane];
+                }
+                if (u < 3) {
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) kk[(u + 1) & 1][j] = kf[((buf * 4 + u + 1) * NG + j) * kWave + lane];
+                }
+                __builtin_amdgcn_sched_barrier(0);
                 f32x4 acc[MT];
 #pragma unroll
                 for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
-                    const bf16x8 f = __builtin_bit_cast(bf16x8, kf[((buf * 4 + u) * NG + j) * kWave + lane]);
+                    const bf16x8 f = __builtin_bit_cast(bf16x8, kk[u & 1][j]);
 #pragma unroll
                     for (int i = 0; i < MT; ++i) acc[i] = mfma(f, qf[i][j], acc[i]);
                 }
@@ -683,17 +693,26 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
                 p[i][1] = weights_frag(x[i], 1);
             }
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
+            for (int g = 0; g < NG; ++g) {
+                if (g == 0) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) vv[0][s] = vf[(buf * 4 * NG + s) * kWave + lane];
+                }
+                if (g + 1 < NG) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) vv[(g + 1) & 1][s] = vf[(buf * 4 * NG + 4 * g + 4 + s) * kWave + lane];
+                }
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const uint4 *f = vf + ((buf * 2 * NG + 2 * g + s) * 2) * kWave + lane;
-                    const bf16x8 e = __builtin_bit_cast(bf16x8, f[0]), o = __builtin_bit_cast(bf16x8, f[kWave]);
+                    const bf16x8 e = __builtin_bit_cast(bf16x8, vv[g & 1][2 * s]), o = __builtin_bit_cast(bf16x8, vv[g & 1][2 * s + 1]);
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
                         oe[i][g] = mfma(e, p[i][s], oe[i][g]);
                         oo[i][g] = mfma(o, p[i][s], oo[i][g]);
                     }
                 }
+            }
         }
         __syncthreads();
     }

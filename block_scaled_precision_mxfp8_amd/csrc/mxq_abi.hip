@@ -734,13 +734,13 @@ mxq_status mxfp4_kv_append(const mxq_kv_cache *cache, const uint16_t *k, int64_t
 
 size_t mxfp4_kv_attention_workspace_size(int32_t seqs, int32_t tokens, int32_t q_heads,
                                          int32_t kv_heads, int32_t head_dim, int32_t page_size,
-                                         int32_t width)
+                                         int32_t width, int32_t window)
 {
-    if (seqs <= 0 || tokens <= 0 || q_heads <= 0 || width <= 0 ||
+    if (seqs <= 0 || tokens <= 0 || q_heads <= 0 || width <= 0 || window < 0 ||
         !kv_shape_ok(kv_heads, head_dim, page_size) || q_heads % kv_heads)
         return 0;
     const int32_t splits =
-        mxq::kv4_attention_splits(seqs, tokens, q_heads, kv_heads, head_dim, page_size, width, 0);
+        mxq::kv4_attention_splits(seqs, tokens, q_heads, kv_heads, head_dim, page_size, width, window);
     if (splits <= 1) return 0;
     return (size_t)splits * seqs * tokens * q_heads * (head_dim + 2) * sizeof(float);
 }
@@ -773,7 +773,7 @@ mxq_status mxfp4_kv_attention(const mxq_kv_cache *cache, const mxq_kv_attention 
         return MXQ_ESIZE;
     const size_t need =
         mxfp4_kv_attention_workspace_size(args->seqs, args->tokens, args->q_heads, a.geo.heads,
-                                          a.geo.dim, a.geo.page, args->width);
+                                          a.geo.dim, a.geo.page, args->width, args->window);
     if (need > 0 && !args->workspace) return MXQ_EINVAL;
     if (args->workspace_bytes < need) return MXQ_ESIZE;
     a.cache = cache->data;

@@ -12,13 +12,17 @@ cache of a model is one uint8 tensor [layers, pages, page_bytes]
 """
 from __future__ import annotations
 
-import ctypes
 import heapq
-import math
+import struct
 
 import torch
 
 import block_scaled_precision_mxfp8_amd as _mxq
+
+# mxq_kv_cache and mxq_kv_attention as bytes: packing them costs a fraction of
+# filling a ctypes structure field by field
+_CACHE = struct.Struct("@Pqqiiii")
+_ATTENTION = struct.Struct("@PqqqPqPiiiifiiiPPPN")
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -30,7 +34,7 @@ def _stream_of(device: torch.device) -> int:
 
 
 def _need(t: torch.Tensor, what: str, dtype: torch.dtype, device: torch.device):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{what} must be a {str(dtype).removeprefix('torch.')} tensor")
     if t.device != device:
         raise ValueError(f"{what} must be on {device}")
@@ -38,9 +42,12 @@ def _need(t: torch.Tensor, what: str, dtype: torch.dtype, device: torch.device):
 
 def _rows16(x: torch.Tensor) -> torch.Tensor:
     """x with a unit last stride and 16-byte aligned rows (a copy if it has none)."""
-    st = x.stride()
-    if st[-1] != 1 or x.data_ptr() % 16 or any(v % 8 for v in st[:-1]):
+    *rows, unit = x.stride()
+    if unit != 1 or x.data_ptr() % 16:
         return x.clone(memory_format=torch.contiguous_format)
+    for v in rows:
+        if v % 8:
+            return x.clone(memory_format=torch.contiguous_format)
     return x
 
 
@@ -142,16 +149,17 @@ def mxfp4_kv_cache(layers: int, pages: int, kv_heads: int, head_dim: int, page_s
                        dtype=torch.uint8, device=device)
 
 
-def _layer(cache: torch.Tensor, kv_heads: int, head_dim: int, page_size: int) -> "_mxq.KVCacheDesc":
-    if not isinstance(cache, torch.Tensor) or cache.dtype != torch.uint8:
+def _layer(cache: torch.Tensor, dev: torch.device, kv_heads: int, head_dim: int, page_size: int) -> bytes:
+    """mxq_kv_cache of one layer."""
+    if not isinstance(cache, torch.Tensor) or cache.dtype is not torch.uint8:
         raise TypeError("cache must be a uint8 tensor")
-    if not cache.is_cuda:
-        raise ValueError("cache must live on the GPU (the library has no CPU path)")
-    nbytes = mxfp4_kv_page_bytes(kv_heads, head_dim, page_size)
-    if cache.dim() != 2 or cache.shape[1] != nbytes or cache.stride(1) != 1:
+    if cache.device != dev:
+        raise ValueError(f"cache must be on {dev}")
+    nbytes = _page_bytes.get((kv_heads, head_dim, page_size)) or mxfp4_kv_page_bytes(kv_heads, head_dim, page_size)
+    shape = cache.shape
+    if len(shape) != 2 or shape[1] != nbytes or cache.stride(1) != 1:
         raise ValueError(f"cache must be one layer, [pages, {nbytes}] bytes for these heads")
-    return _mxq.KVCacheDesc(cache.data_ptr(), cache.shape[0], cache.stride(0), kv_heads, head_dim,
-                            page_size, 0)
+    return _CACHE.pack(cache.data_ptr(), shape[0], cache.stride(0), kv_heads, head_dim, page_size, 0)
 
 
 def mxfp4_kv_append(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
@@ -166,23 +174,23 @@ def mxfp4_kv_append(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots
     dev = k.device
     _need(v, "v", torch.bfloat16, dev)
     _need(slots, "slots", torch.int64, dev)
-    if k.dim() != 3 or v.shape != k.shape:
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape:
         raise ValueError("k and v must be [tokens, kv_heads, head_dim]")
-    tokens, heads, dim = k.shape
-    if slots.dim() != 1 or slots.shape[0] != tokens:
+    tokens, heads, dim = shape
+    if slots.shape != (tokens,):
         raise ValueError("slots must be [tokens]")
-    desc = _layer(cache, heads, dim, page_size)
-    if cache.device != dev:
-        raise ValueError(f"cache must be on {dev}")
+    desc = _layer(cache, dev, heads, dim, page_size)
     k, v, slots = _rows16(k), _rows16(v), slots.contiguous()
     kq = vq = None
+    kp = vp = 0
     if fake_quant:
-        kq = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=dev)
-        vq = torch.empty_like(kq)
-    st = _mxq.load().mxfp4_kv_append(
-        ctypes.byref(desc), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-        v.stride(1), slots.data_ptr(), tokens, kq.data_ptr() if fake_quant else None,
-        vq.data_ptr() if fake_quant else None, _stream_of(dev))
+        kq, vq = k.new_empty(shape), k.new_empty(shape)
+        kp, vp = kq.data_ptr(), vq.data_ptr()
+    ks, vs = k.stride(), v.stride()
+    st = (_mxq._lib or _mxq.load()).mxfp4_kv_append(
+        desc, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], slots.data_ptr(), tokens, kp,
+        vp, _stream_of(dev))
     if st:
         raise _mxq.MXQError("mxfp4_kv_append", st)
     return (kq, vq) if fake_quant else None
@@ -207,37 +215,37 @@ def mxfp4_kv_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.T
     dev = q.device
     _need(page_table, "page_table", torch.int32, dev)
     _need(lengths, "lengths", torch.int32, dev)
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q must be [seqs, tokens, q_heads, head_dim]")
-    seqs, tokens, heads, dim = q.shape
-    if page_table.dim() != 2 or page_table.shape[0] != seqs:
+    seqs, tokens, heads, dim = shape
+    table_shape = page_table.shape
+    if len(table_shape) != 2 or table_shape[0] != seqs:
         raise ValueError("page_table must be [seqs, width]")
-    if lengths.dim() != 1 or lengths.shape[0] != seqs:
+    if lengths.shape != (seqs,):
         raise ValueError("lengths must be [seqs]")
     if kv_heads < 1 or heads < 1 or heads % kv_heads:
         raise ValueError("q's heads must be a multiple of kv_heads")
     if window < 0:
         raise ValueError("window must not be negative")
-    desc = _layer(cache, kv_heads, dim, page_size)
-    if cache.device != dev:
-        raise ValueError(f"cache must be on {dev}")
+    desc = _layer(cache, dev, kv_heads, dim, page_size)
     q = _rows16(q)
-    if page_table.stride(1) != 1 or page_table.stride(0) < page_table.shape[1]:
+    width = table_shape[1]
+    row, unit = page_table.stride()
+    if unit != 1 or row < width:
         page_table = page_table.contiguous()
+        row = width
     lengths = lengths.contiguous()
-    width = page_table.shape[1]
-    out = torch.empty((seqs, tokens, heads, dim), dtype=torch.bfloat16, device=dev)
-    lse = torch.empty((seqs, tokens, heads), dtype=torch.float32, device=dev) if return_lse else None
-    L = _mxq.load()
-    nbytes = L.mxfp4_kv_attention_workspace_size(seqs, tokens, heads, kv_heads, dim, page_size, width)
-    ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
+    out = q.new_empty(shape)
+    lse = q.new_empty(shape[:3], dtype=torch.float32) if return_lse else None
+    L = _mxq._lib or _mxq.load()
+    nbytes = L.mxfp4_kv_attention_workspace_size(seqs, tokens, heads, kv_heads, dim, page_size, width, window)
+    ws = q.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
     s0, s1, s2, _ = q.stride()
-    args = _mxq.KVAttentionArgs(
-        q.data_ptr(), s0, s1, s2, page_table.data_ptr(), max(page_table.stride(0), width),
-        lengths.data_ptr(), seqs, tokens, heads, width,
-        1.0 / math.sqrt(dim) if scale is None else scale, bool(causal), window, 0, out.data_ptr(),
-        lse.data_ptr() if return_lse else None, ws.data_ptr() if nbytes else None, nbytes)
-    st = L.mxfp4_kv_attention(ctypes.byref(desc), ctypes.byref(args), _stream_of(dev))
+    st = L.mxfp4_kv_attention(desc, _ATTENTION.pack(
+        q.data_ptr(), s0, s1, s2, page_table.data_ptr(), row, lengths.data_ptr(), seqs, tokens, heads,
+        width, dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, 0, out.data_ptr(),
+        lse.data_ptr() if return_lse else 0, ws.data_ptr() if nbytes else 0, nbytes), _stream_of(dev))
     if st:
         raise _mxq.MXQError("mxfp4_kv_attention", st)
     return (out, lse) if return_lse else out
@@ -267,7 +275,7 @@ def mxfp4_kv_copy_pages(cache: torch.Tensor, src: torch.Tensor, dst: torch.Tenso
         raise ValueError("cache must be [layers, pages, page_bytes]")
     if last != 1:
         raise ValueError("a page must be contiguous")
-    st = _mxq.load().mxfp4_kv_copy_pages(
+    st = (_mxq._lib or _mxq.load()).mxfp4_kv_copy_pages(
         cache.data_ptr(), layers, layer_stride, pages, page_stride, nbytes,
         src.contiguous().data_ptr(), dst.contiguous().data_ptr(), src.shape[0], _stream_of(dev))
     if st:

@@ -570,7 +570,7 @@ typedef struct mxq_kv_attention {
 
 size_t mxfp4_kv_attention_workspace_size(int32_t seqs, int32_t tokens, int32_t q_heads,
                                          int32_t kv_heads, int32_t head_dim, int32_t page_size,
-                                         int32_t width);
+                                         int32_t width, int32_t window);
 
 mxq_status mxfp4_kv_attention(const mxq_kv_cache *cache, const mxq_kv_attention *args,
                               void *stream);

@@ -108,12 +108,13 @@ def test_attention_refusals(lib):
     assert f(desc(), seqs=0, q=None, out=None) == mxq.MXQ_OK
     assert f(desc(), tokens=0, q=None, out=None) == mxq.MXQ_OK
     size = lib.mxfp4_kv_attention_workspace_size
-    need = size(1, 1, 32, 8, 128, 64, 1024)
+    need = size(1, 1, 32, 8, 128, 64, 1024, 0)
     assert need > 0
     kw = dict(seqs=1, width=1024, table_stride=1024)
     assert f(desc(), workspace_bytes=need - 1, **kw) == mxq.MXQ_ESIZE
     assert f(desc(), workspace=None, **kw) == mxq.MXQ_EINVAL
-    assert size(0, 1, 32, 8, 128, 64, 4) == 0 and size(1, 1, 32, 5, 128, 64, 4) == 0 and size(1, 1, 32, 8, 80, 64, 4) == 0
+    assert size(0, 1, 32, 8, 128, 64, 4, 0) == 0 and size(1, 1, 32, 5, 128, 64, 4, 0) == 0 and size(1, 1, 32, 8, 80, 64, 4, 0) == 0
+    assert size(1, 1, 32, 8, 128, 64, 1024, -1) == 0 and size(1, 1, 32, 8, 128, 64, 1024, 256) == 0
 
 
 def test_copy_refusals(lib):

@@ -198,6 +198,42 @@ def test_append(gpu, orc, geo, tokens):
                 assert got is None
 
 
+@pytest.mark.parametrize("geo", [(16, 64, 16), (32, 96, 48), (16, 128, 64), (16, 192, 32), (16, 256, 16)], ids=str)
+def test_append_long_runs(gpu, orc, geo):
+    """A prompt of several sequences: runs that begin and end inside blocks of 16, with gaps."""
+    heads, dim, page = geo
+    announce(f"append long runs {geo}")
+    rng = np.random.default_rng(dim)
+    tokens = 32768 // heads + 37
+    pages = tokens // page + 40
+    slots, where = [], 0
+    order = rng.permutation(pages)
+    while len(slots) < tokens:
+        run = int(rng.integers(1, 400))
+        first = where * page + int(rng.integers(0, page))
+        place = np.arange(first, first + run)
+        place = order[place // page % pages] * page + place % page
+        slots += place.tolist()
+        where += -(-(first % page + run) // page)
+        if where >= pages - 400 // page - 2:
+            where = 0
+    slots = np.array(slots[:tokens], np.int64)
+    seen, keep = set(), np.ones(tokens, bool)
+    for i, v in enumerate(slots.tolist()):
+        keep[i] = v not in seen
+        seen.add(v)
+    slots[~keep] = -1  # a place is used once
+    xb = bf16_bits(rng.standard_normal((tokens, 2 * heads, dim)))
+    x = to_dev_bf16(xb)
+    cache = gpu.mxfp4_kv_cache(1, pages, heads, dim, page)[0]
+    gpu.mxfp4_kv_append(cache, x[:, :heads], x[:, heads:], torch.from_numpy(slots).cuda(), page)
+    want = np.zeros(cache.shape, np.uint8)
+    q, s = orc.mxfp4_quantize(xb.reshape(-1, dim))
+    q, s = q.reshape(tokens, 2 * heads, -1), s.reshape(tokens, 2 * heads, -1)
+    ref.write_page_tokens(want, geo, slots, q[:, :heads], s[:, :heads], q[:, heads:], s[:, heads:])
+    assert np.array_equal(u8(cache), want)
+
+
 def test_append_nothing_and_strides(gpu, orc):
     announce("append nothing, odd strides")
     heads, dim, page = 2, 64, 16
