@@ -57,16 +57,24 @@ __device__ __forceinline__ uint32_t has_ff(uint32_t w)
     return (~w - 0x01010101u) & w & 0x80808080u;
 }
 
+// Over the four lanes of a column, kg = 0..3 (lanes 16 apart), by swaps of half
+// and quarter waves: no trip through LDS, which costs some 130 clocks each.
 __device__ __forceinline__ float max_over_kg(float v)
 {
-    v = fmaxf(v, __shfl_xor(v, 16, kWave));
-    return fmaxf(v, __shfl_xor(v, 32, kWave));
+    const uint32_t u = __float_as_uint(v);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t w = __float_as_uint(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+    const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
 __device__ __forceinline__ float sum_over_kg(float v)
 {
-    v += __shfl_xor(v, 16, kWave);
-    return v + __shfl_xor(v, 32, kWave);
+    const uint32_t u = __float_as_uint(v);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t w = __float_as_uint(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -464,8 +472,16 @@ __global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(Kv4Attn a)
 // Many rows: eight waves of MT x 16 rows each share the tiles.  A tile's K and V
 // are decoded once, an eighth by each wave, into LDS as whole matrix operands
 // (1 KiB each, lane by lane, so that reads and writes are free of conflicts),
-// two tiles deep: while one is multiplied the next is decoded and the one
-// after it is on its way from memory.  One barrier a tile.
+// two buffers deep: while a tile is multiplied the next is decoded, and the
+// codes of the two after it are on their way from memory.  One barrier a tile.
+//
+// Bound by issue: 512 query tokens over 12..16 k cached tokens (2 sequences, 32
+// query heads on 8 kv heads of 128; 234 GFLOP) take 278 us; a tile costs a wave
+// some 300 vector and 64 matrix instructions, which the two waves of a SIMD,
+// kept together by the barrier, hardly overlap: the products alone take 135
+// us.  Waves 4..7 half a tile behind the others (two barriers a tile) took 342
+// us, MT = 1 328, one tile less in flight 291, no reads ahead of the products
+// in LDS 308.
 // ---------------------------------------------------------------------------
 constexpr int kShareWaves = 8;
 
@@ -523,10 +539,12 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
     const int rot = (8 * (m & 3) + 9) & 31;
     Block kb, vb;
     int k_page = -1, v_page = -1;
-    uint32_t kc[kHalf], ks[scale_sets(D)];
-    uint2 vc[kVRounds], vs[kVRounds];
-    bool v_ok = false;
-    auto load = [&]() {  // the tile the blocks stand at; then on to the next
+    struct Share {  // of one tile
+        uint32_t kc[kHalf], ks[scale_sets(D)];
+        uint2 vc[kVRounds], vs[kVRounds];
+        bool v_ok;
+    } share[2];
+    auto load = [&](Share &t) {  // the tile the blocks stand at; then on to the next
         {
             const bool ok = k_page >= 0 && k_page < a.geo.pages;
             const uint8_t *base = a.cache + (ok ? k_page : 0) * a.geo.page_stride;
@@ -534,25 +552,25 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
             if (NG % 2 == 0 || kn == kHalf) {
                 const Words<kHalf> v = *reinterpret_cast<const Words<kHalf> *>(p);
 #pragma unroll
-                for (int j = 0; j < kHalf; ++j) kc[j] = v.w[j];
+                for (int j = 0; j < kHalf; ++j) t.kc[j] = v.w[j];
             } else {
 #pragma unroll
-                for (int j = 0; j < kHalf; ++j) kc[j] = j < kn ? reinterpret_cast<const uint32_t *>(p)[j] : 0u;
+                for (int j = 0; j < kHalf; ++j) t.kc[j] = j < kn ? reinterpret_cast<const uint32_t *>(p)[j] : 0u;
             }
             // the group of this wave's first dim of the lane, and the one after it
             const int g0 = D == 256 ? 2 * kg + (wave & 1) : kg * (D / 4) / 32;
             const uint8_t *sp = base + a.geo.k_scales() + a.geo.scale(h, kb.in * 16, g0) + 4 * ku;
-            ks[0] = ld4<false>(sp);
-            if constexpr (scale_sets(D) == 2) ks[1] = D == 256 ? ks[0] : ld4<false>(sp + (g0 + 1 < NG ? 16 : 0));
+            t.ks[0] = ld4<false>(sp);
+            if constexpr (scale_sets(D) == 2) t.ks[1] = D == 256 ? t.ks[0] : ld4<false>(sp + (g0 + 1 < NG ? 16 : 0));
         }
-        v_ok = v_page >= 0 && v_page < a.geo.pages;
-        const uint8_t *base = a.cache + (v_ok ? v_page : 0) * a.geo.page_stride;
+        t.v_ok = v_page >= 0 && v_page < a.geo.pages;
+        const uint8_t *base = a.cache + (t.v_ok ? v_page : 0) * a.geo.page_stride;
 #pragma unroll
         for (int r = 0; r < kVRounds; ++r) {
             const int unit = wave + kShareWaves * r, g = unit >> 1, s = unit & 1;
             if (unit < 2 * NG) {
-                vc[r] = ld8<false>(base + a.geo.v_codes() + a.geo.v_code(h, vb.in * 16, 16 * g + m) + 8 * s);
-                vs[r] = ld8<false>(base + a.geo.v_scales() + a.geo.scale(h, vb.in * 16, g) + 8 * s);
+                t.vc[r] = ld8<false>(base + a.geo.v_codes() + a.geo.v_code(h, vb.in * 16, 16 * g + m) + 8 * s);
+                t.vs[r] = ld8<false>(base + a.geo.v_scales() + a.geo.scale(h, vb.in * 16, g) + 8 * s);
             }
         }
         kb.advance(step_pages, step_blocks, bpp);
@@ -563,31 +581,31 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
     auto masked = [&](int tile, bool ok) {
         return tile * 64 < see.all_lo || tile * 64 + 64 > see.all_hi || wave_any(!ok);
     };
-    auto decode = [&](int tile, int buf) {
+    auto decode = [&](Share &sh, int tile, int buf) {
 #pragma unroll
         for (int j = 0; j < kHalf; ++j) {
             if (j < kn) {
-                uint32_t w = ks[0];
+                uint32_t w = sh.ks[0];
                 if constexpr (scale_sets(D) == 2)
-                    w = D == 256 || 8 * (kj + j) + kg * (D / 4) % 32 < 32 ? ks[0] : ks[1];
-                const bf16x8 f = fp4_frag(kc[j], __builtin_amdgcn_alignbit(w, w, rot));
+                    w = D == 256 || 8 * (kj + j) + kg * (D / 4) % 32 < 32 ? sh.ks[0] : sh.ks[1];
+                const bf16x8 f = fp4_frag(sh.kc[j], __builtin_amdgcn_alignbit(w, w, rot));
                 kf[((buf * 4 + ku) * NG + kj + j) * kWave + lane] = __builtin_bit_cast(uint4, f);
             }
         }
-        const bool mask = masked(tile, v_ok);
+        const bool mask = masked(tile, sh.v_ok);
 #pragma unroll
         for (int r = 0; r < kVRounds; ++r) {
             const int unit = wave + kShareWaves * r, g = unit >> 1, s = unit & 1;
             if (unit < 2 * NG) {
                 if (mask) {  // scales of tokens no row sees, and NaN scales, leave the product
                     const int first = tile * 64 + 16 * kg + 8 * s;
-                    const int lo = v_ok ? see.any_lo - first : 8, hi = see.any_hi - first;
-                    vs[r].x &= low_bytes(hi) & ~low_bytes(lo);
-                    vs[r].y &= low_bytes(hi - 4) & ~low_bytes(lo - 4);
+                    const int lo = sh.v_ok ? see.any_lo - first : 8, hi = see.any_hi - first;
+                    sh.vs[r].x &= low_bytes(hi) & ~low_bytes(lo);
+                    sh.vs[r].y &= low_bytes(hi - 4) & ~low_bytes(lo - 4);
                     uint32_t nan = 0;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        uint32_t &w = i < 4 ? vs[r].x : vs[r].y;
+                        uint32_t &w = i < 4 ? sh.vs[r].x : sh.vs[r].y;
                         const uint32_t byte = 0xFFu << (8 * (i & 3));
                         if ((w & byte) == byte) {
                             w &= ~byte;
@@ -597,7 +615,7 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
                     if (m == 0) nan_tokens[buf][g][2 * kg + s] = nan;
                 }
                 bf16x8 e, o;
-                v_frags(vc[r].x, vc[r].y, vs[r].x, vs[r].y, e, o);
+                v_frags(sh.vc[r].x, sh.vc[r].y, sh.vs[r].x, sh.vs[r].y, e, o);
                 uint4 *p = vf + ((buf * 2 * NG + unit) * 2) * kWave + lane;
                 p[0] = __builtin_bit_cast(uint4, e);
                 p[kWave] = __builtin_bit_cast(uint4, o);
@@ -611,20 +629,20 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
         vb.start(begin * 4 + kg, bpp);
         k_page = kb.look(table, a.width);
         v_page = vb.look(table, a.width);
-        load();
-        ok_next = v_ok;
-        decode(begin, 0);
-        if (begin + 1 < end) load();
+        load(share[0]);
+        load(share[1]);
+        ok_next = share[0].v_ok;
+        decode(share[0], begin, 0);
+        load(share[0]);
     }
     __syncthreads();
     const bool work = row0 < rows;  // a wave without rows only decodes
-    for (int tile = begin; tile < end; ++tile) {
-        const int buf = (tile - begin) & 1;
+    auto step = [&](int tile, int buf) {
         ok = ok_next;
         if (tile + 1 < end) {
-            ok_next = v_ok;
-            decode(tile + 1, buf ^ 1);
-            if (tile + 2 < end) load();
+            ok_next = share[buf ^ 1].v_ok;
+            decode(share[buf ^ 1], tile + 1, buf ^ 1);
+            load(share[buf ^ 1]);
         }
         if (work) {
             float x[MT][16];  // tokens 16 kg + 0..15 of the tile
@@ -715,6 +733,10 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
             }
         }
         __syncthreads();
+    };
+    for (int tile = begin; tile < end; tile += 2) {
+        step(tile, 0);
+        if (tile + 1 < end) step(tile + 1, 1);
     }
 
     // lane (m, kg) holds dims 32 g + 8 kg + 0..7 of row m
