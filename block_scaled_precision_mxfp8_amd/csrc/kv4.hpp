@@ -61,6 +61,7 @@ struct Kv4Attn {
     // (maximum, sum) pairs [rows, 2] of the softmax in powers of two
     float *part;
     int32_t splits;
+    int32_t ranked;  // start sequences longest first (set by the launcher)
 };
 
 hipError_t launch_kv4_append(const Kv4Geom &geo, uint8_t *cache, const uint16_t *k, int64_t k_tok,

@@ -256,17 +256,47 @@ __device__ __forceinline__ void v_frags(uint32_t c0, uint32_t c1, uint32_t s0, u
     odd = as_bf16x8(o[0], o[1], o[2], o[3]);
 }
 
+// Sequences are started longest first when the workgroups do not all fit at
+// once, so that the last to run are short: the sequence of rank `r` by length,
+// ties in order.  For at most kRanked sequences; with more of them there are
+// enough workgroups to even out.
+constexpr int kRanked = 128;
+
+template <int kThreads>
+__device__ __forceinline__ int sequence_of_rank(const Kv4Attn &a, int r)
+{
+    __shared__ int length[kRanked], rank[kRanked], found;
+    const int t = threadIdx.x % kRanked, part = threadIdx.x / kRanked, parts = kThreads / kRanked;
+    if (part == 0 && t < a.seqs) {
+        length[t] = context_length(a, t);
+        rank[t] = 0;
+    }
+    __syncthreads();
+    if (t < a.seqs) {
+        const int mine = length[t];
+        int before = 0;
+#pragma unroll 4
+        for (int j = part; j < a.seqs; j += parts) before += length[j] > mine || (length[j] == mine && j < t);
+        atomicAdd(&rank[t], before);
+    }
+    __syncthreads();
+    if (part == 0 && t < a.seqs && rank[t] == r) found = t;
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(found);
+}
+
 // kWaves waves take the 64-token tiles of one split in turn, each with its own
 // running maximum and sum, and are joined through LDS in a fixed order.
 template <int D, int kWaves>
-__global__ __launch_bounds__(kWaves * 64) void kv4_attention_kernel(Kv4Attn a)
+__global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attention_kernel(Kv4Attn a)
 {
     constexpr int NG = D / 32;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int m = lane & 15, kg = lane >> 4;
     const int heads = a.geo.heads, group = a.q_heads / heads, T = a.tokens;
-    const int h = blockIdx.x % heads, b = blockIdx.x / heads, split = blockIdx.z;
+    const int h = blockIdx.x % heads, split = blockIdx.z;
+    const int b = a.ranked ? sequence_of_rank<kWaves * kWave>(a, blockIdx.x / heads) : blockIdx.x / heads;
     const int rows = T * group, row0 = blockIdx.y * 16;
 
     const int len = context_length(a, b);
@@ -819,8 +849,13 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(const float *__restrict__
     if (lse && t == 0) lse[line] = (top + __builtin_log2f(total)) * kLn2;
 }
 
-// Waves of a workgroup.  Eight as long as their registers fit (256 each).
-constexpr int waves_for(int dim) { return dim <= 128 ? 8 : 4; }
+// Waves of a workgroup of the few-row kernel.  Eight finish a sequence sooner
+// and need fewer splits; four (three workgroups a CU up to 128 dims, whose
+// beginnings and ends then overlap) do better once there are that many.  128
+// sequences of 0..4096 tokens, 8 heads of 128: 66 us with eight, 57 with four;
+// 64 of 4096..8192: 79 and 80; 48 of 0..8192: 48 and 71.
+constexpr int kFewWaves = 8;
+constexpr int64_t kManyGroups = 768;
 
 // Row tiles of a wave of the many-row kernel.
 constexpr int row_tiles(int dim, int64_t rows) { return dim <= 128 && rows > 128 ? 2 : 1; }
@@ -828,6 +863,8 @@ constexpr int row_tiles(int dim, int64_t rows) { return dim <= 128 && rows > 128
 // Rows (query tokens x query heads of one kv head) from which K and V are
 // decoded once for all.
 constexpr int64_t kManyRows = 33;
+
+constexpr int64_t kCus = 256;
 
 template <int D, int MT>
 hipError_t go_rows(const Kv4Attn &a, int64_t rows, hipStream_t stream)
@@ -839,10 +876,19 @@ hipError_t go_rows(const Kv4Attn &a, int64_t rows, hipStream_t stream)
     return hipGetLastError();
 }
 
+template <int D, int kWaves>
+hipError_t go_few(const Kv4Attn &a, int64_t gx, int64_t gy, hipStream_t stream)
+{
+    Kv4Attn ordered = a;
+    ordered.ranked = a.seqs > 1 && a.seqs <= kRanked && gx * gy * a.splits > kCus;
+    hipLaunchKernelGGL((kv4_attention_kernel<D, kWaves>), dim3((unsigned)gx, (unsigned)gy, (unsigned)a.splits),
+                       dim3(kWaves * kWave), 0, stream, ordered);
+    return hipGetLastError();
+}
+
 template <int D>
 hipError_t go(const Kv4Attn &a, hipStream_t stream)
 {
-    constexpr int kWaves = waves_for(D);
     const int64_t rows = (int64_t)a.tokens * (a.q_heads / a.geo.heads);
     const int64_t gx = (int64_t)a.seqs * a.geo.heads, lines = (int64_t)a.seqs * a.tokens * a.q_heads;
     if (gx > 0x7FFFFFFF || lines > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
@@ -850,9 +896,9 @@ hipError_t go(const Kv4Attn &a, hipStream_t stream)
     if (rows >= kManyRows) {
         e = row_tiles(D, rows) == 2 ? go_rows<D, D <= 128 ? 2 : 1>(a, rows, stream) : go_rows<D, 1>(a, rows, stream);
     } else {
-        hipLaunchKernelGGL((kv4_attention_kernel<D, kWaves>), dim3((unsigned)gx, (unsigned)((rows + 15) / 16), (unsigned)a.splits),
-                           dim3(kWaves * kWave), 0, stream, a);
-        e = hipGetLastError();
+        const int64_t gy = (rows + 15) / 16;
+        e = D <= 128 && gx * gy * a.splits >= kManyGroups ? go_few<D, D <= 128 ? 4 : kFewWaves>(a, gx, gy, stream)
+                                                          : go_few<D, kFewWaves>(a, gx, gy, stream);
     }
     if (e != hipSuccess || a.splits == 1) return e;
     hipLaunchKernelGGL((kv4_join_kernel<D>), dim3((unsigned)lines), dim3(256), 0, stream, a.part, lines,
@@ -863,8 +909,10 @@ hipError_t go(const Kv4Attn &a, hipStream_t stream)
 }  // namespace
 
 // Splitting the context fills the CUs when there are few rows, but costs a
-// second launch and the partial sums; a wave (with few rows) should have two
-// tiles at least, a workgroup with many rows eight.
+// second launch and the partial sums, in all about the time of three or four
+// tiles (2 us each, alone): up to four tiles a wave there is one split, else no
+// less than one tile for a wave (with many rows, eight for the workgroup).
+// Seven sequences that see 1088 tokens: 11 us in one call, 16 with two splits.
 int32_t kv4_attention_splits(int64_t seqs, int64_t tokens, int64_t q_heads, int64_t kv_heads,
                              int64_t dim, int64_t page, int64_t width, int64_t window)
 {
@@ -874,8 +922,9 @@ int32_t kv4_attention_splits(int64_t seqs, int64_t tokens, int64_t q_heads, int6
     const int64_t groups = (rows + tile - 1) / tile * seqs * kv_heads;
     int64_t seen = width * page;
     if (window > 0 && window + tokens + 64 < seen) seen = window + tokens + 64;
-    const int64_t fill = (256 + groups - 1) / groups;  // a workgroup per CU
-    const int64_t most = (seen + 63) / 64 / (many ? 8 : 2 * waves_for((int)dim));
+    const int64_t fill = (kCus + groups - 1) / groups;  // a workgroup per CU
+    const int64_t tiles = (seen + 63) / 64;
+    const int64_t most = many ? tiles / 8 : tiles > 4 * kFewWaves ? tiles / kFewWaves : 1;
     const int64_t s = fill < most ? fill : most;
     return (int32_t)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
 }

@@ -290,6 +290,22 @@ def test_attention(gpu, geo, tokens, group):
         attend(gpu, geo, cache, host, q, table, lengths, causal=causal, window=window)
 
 
+@pytest.mark.parametrize("seqs,geo", [(100, (8, 64, 16)), (130, (7, 96, 48)), (100, (8, 128, 32)), (40, (8, 128, 32)), (40, (8, 192, 32)),
+                                      (128, (3, 256, 16))], ids=str)
+def test_attention_many_sequences(gpu, seqs, geo):
+    """More workgroups than CUs: sequences are started by length, ties among them."""
+    heads, dim, page = geo
+    announce(f"attention {seqs} sequences {geo}")
+    rng = np.random.default_rng(seqs + dim)
+    cache, host = filled_cache(rng, geo, 50)
+    lengths = rng.integers(0, 180, seqs).astype(np.int32)
+    lengths[: seqs // 4] = 77
+    table = rng.integers(0, 50, (seqs, -(-180 // page)), dtype=np.int32)
+    q = to_dev_bf16(bf16_bits(rng.standard_normal((seqs, 1, heads * 2, dim))))
+    attend(gpu, geo, cache, host, q, table, lengths)
+    attend(gpu, geo, cache, host, q, table, lengths, window=40)
+
+
 @pytest.mark.parametrize("width,lengths", [(3, [500, 48, -5]), (0, [4, 0, 9]), (40, [1, 640, 639])])
 def test_attention_lengths_and_holes(gpu, width, lengths):
     """Lengths past the table or below zero, an empty table, holes in it, no pages at all."""
