@@ -97,65 +97,99 @@ __device__ __forceinline__ Words<NG> load_once(const uint8_t *p)
 
 constexpr int scale_sets(int dim) { return dim == 64 || dim == 128 ? 1 : 2; }
 
-// The place of a lane's block of 16 tokens: entry of the page table, block in
-// the page, advanced by a constant number of blocks without a division.
-struct Block {
-    int page, in;
-    __device__ __forceinline__ void start(int blk, int per_page)
+// Where a tile lies.  In general each block of 16 tokens may be in a page of its
+// own, and a lane follows the block it loads from.  With pages of a multiple of
+// 64 tokens (kWide) a tile is in one page: place and address are then the same
+// for the whole wave, kept in scalar registers, and a lane only adds an offset
+// that never changes.
+template <bool kWide>
+struct Place {
+    int entry, in;  // of the page table, block in the page
+    int loaded;     // the table's entry, -1 for none: read ahead, looked at when used
+    __device__ __forceinline__ void start(const Kv4Attn &a, const int32_t *table, int per_page, int tile, int block)
     {
-        page = blk / per_page;
-        in = blk - page * per_page;
+        const int blk = tile * 4 + (kWide ? 0 : block);
+        entry = blk / per_page;
+        in = blk - entry * per_page;
+        look(a, table);
     }
-    __device__ __forceinline__ void advance(int pages, int blocks, int per_page)
+    __device__ __forceinline__ void advance(const Kv4Attn &a, const int32_t *table, int entries, int blocks, int per_page)
     {
-        page += pages;
+        entry += entries;
         in += blocks;
         if (in >= per_page) {
             in -= per_page;
-            ++page;
+            ++entry;
         }
+        look(a, table);
     }
-    // its page, -1 for none
-    __device__ __forceinline__ int look(const int32_t *table, int width) const
+    __device__ __forceinline__ void look(const Kv4Attn &a, const int32_t *table)
     {
-        return page < width ? table[page] : -1;
+        loaded = entry < a.width ? table[entry] : -1;
+    }
+    __device__ __forceinline__ int page() const
+    {
+        return kWide ? __builtin_amdgcn_readfirstlane(loaded) : loaded;
+    }
+    __device__ __forceinline__ bool ok(const Kv4Attn &a) const { return page() >= 0 && page() < a.geo.pages; }
+    // Its page; page 0 stands in for one not in the cache, whose tokens are masked.
+    __device__ __forceinline__ const uint8_t *base(const Kv4Attn &a) const
+    {
+        return a.cache + (int64_t)(ok(a) ? page() : 0) * a.geo.page_stride;
     }
 };
 
+// Bytes of a block of 16 tokens of one head, in codes and in scales; offsets in
+// a page fit 32 bits.
+constexpr int code_block(int dim) { return 8 * dim; }
+constexpr int scale_block(int dim) { return dim / 2; }
+
 // What a lane loads of K: codes of its four tokens, the scales of their block.
-template <int D>
+template <int D, bool kWide>
 struct KTile {
     static constexpr int NG = D / 32;
     Words<NG> codes[4];
     uint4 scales[scale_sets(D)];  // the groups its D / 4 dims touch
+    uint32_t code_at, scale_at;   // in the page, from the tile's (or its block's) first token
 
-    __device__ __forceinline__ void load(const uint8_t *cache, const Kv4Geom &geo, int h, int page, int in, int m, int kg)
+    __device__ __forceinline__ void init(const Kv4Geom &geo, int h, int m, int kg)
     {
-        const bool ok = page >= 0 && page < geo.pages;
-        const uint8_t *base = cache + (ok ? page : 0) * geo.page_stride;
-        const uint8_t *kc = base + geo.k_code(h, in * 16 + (m & 3)) + kg * (D / 8);
+        const int first = kWide ? 16 * (m >> 2) : 0;
+        code_at = (uint32_t)(geo.k_code(h, first + (m & 3)) + kg * (D / 8));
+        scale_at = (uint32_t)(geo.k_scales() + geo.scale(h, first, kg * (D / 4) / 32));
+    }
+    __device__ __forceinline__ void load(const Kv4Attn &a, const Place<kWide> &at, int kg)
+    {
+        const uint8_t *base = at.base(a);
+        const uint8_t *kc = base + at.in * code_block(D) + code_at;
 #pragma unroll
         for (int u = 0; u < 4; ++u) codes[u] = load_once<NG>(kc + u * 4 * (D / 2));
-        const int g0 = kg * (D / 4) / 32;
-        const uint8_t *ks = base + geo.k_scales() + geo.scale(h, in * 16, g0);
+        const uint8_t *ks = base + at.in * scale_block(D) + scale_at;
         scales[0] = ld16<false>(ks);
-        if constexpr (scale_sets(D) == 2) scales[1] = ld16<false>(ks + (g0 + 1 < NG ? 16 : 0));
+        if constexpr (scale_sets(D) == 2) scales[1] = ld16<false>(ks + (kg * (D / 4) / 32 + 1 < NG ? 16 : 0));
     }
 };
 
 // Of V: codes of 16 tokens x NG dim pairs and their scales.
-template <int D>
+template <int D, bool kWide>
 struct VTile {
     static constexpr int NG = D / 32;
     uint4 codes[NG], scales[NG];
+    uint32_t code_at, scale_at;
     bool ok;  // the block's page is in the cache
 
-    __device__ __forceinline__ void load(const uint8_t *cache, const Kv4Geom &geo, int h, int page, int in, int m)
+    __device__ __forceinline__ void init(const Kv4Geom &geo, int h, int m, int kg)
     {
-        ok = page >= 0 && page < geo.pages;
-        const uint8_t *base = cache + (ok ? page : 0) * geo.page_stride;
-        const uint8_t *vc = base + geo.v_codes() + geo.v_code(h, in * 16, m);
-        const uint8_t *vs = base + geo.v_scales() + geo.scale(h, in * 16, 0);
+        const int first = kWide ? 16 * kg : 0;
+        code_at = (uint32_t)(geo.v_codes() + geo.v_code(h, first, m));
+        scale_at = (uint32_t)(geo.v_scales() + geo.scale(h, first, 0));
+    }
+    __device__ __forceinline__ void load(const Kv4Attn &a, const Place<kWide> &at)
+    {
+        ok = at.ok(a);
+        const uint8_t *base = at.base(a);
+        const uint8_t *vc = base + at.in * code_block(D) + code_at;
+        const uint8_t *vs = base + at.in * scale_block(D) + scale_at;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             codes[g] = ld16<true>(vc + g * 256);
@@ -287,7 +321,7 @@ __device__ __forceinline__ int sequence_of_rank(const Kv4Attn &a, int r)
 
 // kWaves waves take the 64-token tiles of one split in turn, each with its own
 // running maximum and sum, and are joined through LDS in a fixed order.
-template <int D, int kWaves>
+template <int D, int kWaves, bool kWide>
 __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attention_kernel(Kv4Attn a)
 {
     constexpr int NG = D / 32;
@@ -329,21 +363,18 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attentio
     const int bpp = a.geo.page >> 4;  // blocks in a page
     const int step_pages = 4 * kWaves / bpp, step_blocks = 4 * kWaves - step_pages * bpp;
     int tile = tile0 + split * per + wave;
-    Block kb, vb;
-    KTile<D> kt;
-    VTile<D> vt;
-    int k_page = -1, v_page = -1;  // of the next tile
+    Place<kWide> kp, vp;  // of the next tile
+    KTile<D, kWide> kt;
+    VTile<D, kWide> vt;
     if (tile < tile_end) {
-        kb.start(tile * 4 + (m >> 2), bpp);
-        vb.start(tile * 4 + kg, bpp);
-        k_page = kb.look(table, a.width);
-        v_page = vb.look(table, a.width);
-        kt.load(a.cache, a.geo, h, k_page, kb.in, m, kg);
-        vt.load(a.cache, a.geo, h, v_page, vb.in, m);
-        kb.advance(step_pages, step_blocks, bpp);
-        vb.advance(step_pages, step_blocks, bpp);
-        k_page = kb.look(table, a.width);
-        v_page = vb.look(table, a.width);
+        kt.init(a.geo, h, m, kg);
+        vt.init(a.geo, h, m, kg);
+        kp.start(a, table, bpp, tile, m >> 2);
+        vp.start(a, table, bpp, tile, kg);
+        kt.load(a, kp, kg);
+        vt.load(a, vp);
+        kp.advance(a, table, step_pages, step_blocks, bpp);
+        vp.advance(a, table, step_pages, step_blocks, bpp);
     }
     // Each operand's registers are loaded anew as soon as they are used: K of
     // the next tile is in flight during the softmax and the second product, V
@@ -367,9 +398,8 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attentio
             for (int r = 0; r < 4; ++r) x[4 * u + r] = acc[r];
         }
         if (more) {
-            kt.load(a.cache, a.geo, h, k_page, kb.in, m, kg);
-            kb.advance(step_pages, step_blocks, bpp);
-            k_page = kb.look(table, a.width);
+            kt.load(a, kp, kg);
+            kp.advance(a, table, step_pages, step_blocks, bpp);
         }
 
         const int first = tile * 64 + 16 * kg;  // the lane's first token
@@ -437,9 +467,8 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attentio
             }
         }
         if (more) {
-            vt.load(a.cache, a.geo, h, v_page, vb.in, m);
-            vb.advance(step_pages, step_blocks, bpp);
-            v_page = vb.look(table, a.width);
+            vt.load(a, vp);
+            vp.advance(a, table, step_pages, step_blocks, bpp);
         }
     }
 
@@ -511,7 +540,8 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attentio
 // kept together by the barrier, hardly overlap: the products alone take 135
 // us.  Waves 4..7 half a tile behind the others (two barriers a tile) took 342
 // us, MT = 1 328, one tile less in flight 291, no reads ahead of the products
-// in LDS 308.
+// in LDS 308; addresses kept in scalar registers, as the few-row kernel has them,
+// 284: fewer instructions, but the waves stay closer together.
 // ---------------------------------------------------------------------------
 constexpr int kShareWaves = 8;
 
@@ -567,18 +597,18 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
     const int bpp = a.geo.page >> 4, step_pages = 4 / bpp, step_blocks = 4 - step_pages * bpp;
     const int ku = wave >> 1, kj = (wave & 1) * kHalf, kn = wave & 1 ? NG - kHalf : kHalf;
     const int rot = (8 * (m & 3) + 9) & 31;
-    Block kb, vb;
-    int k_page = -1, v_page = -1;
+    Place<false> kp, vp;  // of the next tile
     struct Share {  // of one tile
         uint32_t kc[kHalf], ks[scale_sets(D)];
         uint2 vc[kVRounds], vs[kVRounds];
         bool v_ok;
     } share[2];
-    auto load = [&](Share &t) {  // the tile the blocks stand at; then on to the next
+    // Past the last tile the loads find some page or none; what they bring is
+    // not used.
+    auto load = [&](Share &t) {
         {
-            const bool ok = k_page >= 0 && k_page < a.geo.pages;
-            const uint8_t *base = a.cache + (ok ? k_page : 0) * a.geo.page_stride;
-            const uint8_t *p = base + a.geo.k_code(h, kb.in * 16 + 4 * ku + (m & 3)) + kg * (D / 8) + 4 * kj;
+            const uint8_t *base = kp.base(a);
+            const uint8_t *p = base + a.geo.k_code(h, kp.in * 16 + 4 * ku + (m & 3)) + kg * (D / 8) + 4 * kj;
             if (NG % 2 == 0 || kn == kHalf) {
                 const Words<kHalf> v = *reinterpret_cast<const Words<kHalf> *>(p);
 #pragma unroll
@@ -589,24 +619,22 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
             }
             // the group of this wave's first dim of the lane, and the one after it
             const int g0 = D == 256 ? 2 * kg + (wave & 1) : kg * (D / 4) / 32;
-            const uint8_t *sp = base + a.geo.k_scales() + a.geo.scale(h, kb.in * 16, g0) + 4 * ku;
+            const uint8_t *sp = base + a.geo.k_scales() + a.geo.scale(h, kp.in * 16, g0) + 4 * ku;
             t.ks[0] = ld4<false>(sp);
             if constexpr (scale_sets(D) == 2) t.ks[1] = D == 256 ? t.ks[0] : ld4<false>(sp + (g0 + 1 < NG ? 16 : 0));
         }
-        t.v_ok = v_page >= 0 && v_page < a.geo.pages;
-        const uint8_t *base = a.cache + (t.v_ok ? v_page : 0) * a.geo.page_stride;
+        t.v_ok = vp.ok(a);
+        const uint8_t *base = vp.base(a);
 #pragma unroll
         for (int r = 0; r < kVRounds; ++r) {
             const int unit = wave + kShareWaves * r, g = unit >> 1, s = unit & 1;
             if (unit < 2 * NG) {
-                t.vc[r] = ld8<false>(base + a.geo.v_codes() + a.geo.v_code(h, vb.in * 16, 16 * g + m) + 8 * s);
-                t.vs[r] = ld8<false>(base + a.geo.v_scales() + a.geo.scale(h, vb.in * 16, g) + 8 * s);
+                t.vc[r] = ld8<false>(base + a.geo.v_codes() + a.geo.v_code(h, vp.in * 16, 16 * g + m) + 8 * s);
+                t.vs[r] = ld8<false>(base + a.geo.v_scales() + a.geo.scale(h, vp.in * 16, g) + 8 * s);
             }
         }
-        kb.advance(step_pages, step_blocks, bpp);
-        vb.advance(step_pages, step_blocks, bpp);
-        k_page = kb.look(table, a.width);
-        v_page = vb.look(table, a.width);
+        kp.advance(a, table, step_pages, step_blocks, bpp);
+        vp.advance(a, table, step_pages, step_blocks, bpp);
     };
     auto masked = [&](int tile, bool ok) {
         return tile * 64 < see.all_lo || tile * 64 + 64 > see.all_hi || wave_any(!ok);
@@ -655,10 +683,8 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
 
     bool ok = true, ok_next = true;  // of this lane's block of the tile multiplied, and of the next
     if (begin < end) {
-        kb.start(begin * 4 + (m >> 2), bpp);
-        vb.start(begin * 4 + kg, bpp);
-        k_page = kb.look(table, a.width);
-        v_page = vb.look(table, a.width);
+        kp.start(a, table, bpp, begin, m >> 2);
+        vp.start(a, table, bpp, begin, kg);
         load(share[0]);
         load(share[1]);
         ok_next = share[0].v_ok;
@@ -871,8 +897,9 @@ hipError_t go_rows(const Kv4Attn &a, int64_t rows, hipStream_t stream)
 {
     const int64_t gx = (int64_t)a.seqs * a.geo.heads, gy = (rows + kShareWaves * MT * 16 - 1) / (kShareWaves * MT * 16);
     if (gx > 0x7FFFFFFF || gy > 65535) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((kv4_attention_rows_kernel<D, MT>), dim3((unsigned)gx, (unsigned)gy, (unsigned)a.splits),
-                       dim3(kShareWaves * kWave), 2 * 8 * (D / 32) * kWave * sizeof(uint4), stream, a);
+    const dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)a.splits), block(kShareWaves * kWave);
+    constexpr unsigned lds = 2 * 8 * (D / 32) * kWave * sizeof(uint4);
+    hipLaunchKernelGGL((kv4_attention_rows_kernel<D, MT>), grid, block, lds, stream, a);
     return hipGetLastError();
 }
 
@@ -881,8 +908,11 @@ hipError_t go_few(const Kv4Attn &a, int64_t gx, int64_t gy, hipStream_t stream)
 {
     Kv4Attn ordered = a;
     ordered.ranked = a.seqs > 1 && a.seqs <= kRanked && gx * gy * a.splits > kCus;
-    hipLaunchKernelGGL((kv4_attention_kernel<D, kWaves>), dim3((unsigned)gx, (unsigned)gy, (unsigned)a.splits),
-                       dim3(kWaves * kWave), 0, stream, ordered);
+    const dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)a.splits), block(kWaves * kWave);
+    if (a.geo.page % 64 == 0)
+        hipLaunchKernelGGL((kv4_attention_kernel<D, kWaves, true>), grid, block, 0, stream, ordered);
+    else
+        hipLaunchKernelGGL((kv4_attention_kernel<D, kWaves, false>), grid, block, 0, stream, ordered);
     return hipGetLastError();
 }
 

@@ -247,7 +247,8 @@ mxq_status fp4_matvec(bool nv, const uint16_t *x, int64_t tokens, int64_t ldx, c
 bool kv_shape_ok(int32_t heads, int32_t dim, int32_t page)
 {
     return heads > 0 && (dim == 64 || dim == 96 || dim == 128 || dim == 192 || dim == 256) &&
-           page > 0 && page % 16 == 0 && page <= 65536;
+           page > 0 && page % 16 == 0 && page <= 65536 &&
+           mxq::Kv4Geom{0, 0, heads, dim, page}.page_bytes() <= 0x7FFFFFFF;
 }
 
 // Checks a cache description (its data pointer only when it has pages).

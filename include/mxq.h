@@ -498,7 +498,8 @@ mxq_status nvfp4_matvec(const uint16_t *x, int64_t tokens, int64_t ldx, const ui
  *   V scales  [kv_heads][page_size/16][head_dim/32][16]  E8M0
  * Scales and codes are those of mxfp4_quantize over a token's head_dim values.
  * Shape: head_dim 64, 96, 128, 192 or 256; page_size a multiple of 16, at most
- * 65536 (MXQ_ESHAPE otherwise).
+ * 65536; a page of less than 2 GiB (MXQ_ESHAPE otherwise).  Attention is
+ * somewhat faster with page_size a multiple of 64.
  */
 typedef struct mxq_kv_cache {
     uint8_t *data; /* page 0 of the layer */
