@@ -81,8 +81,10 @@ struct MatvecArgs {
 // / 16, lane / 4 % 4, lane % 4) holds 16 of them, k = 128 kg + 32 p .. of a
 // step of 512: one MXFP4 group, and exactly what four products want, with no
 // exchange between lanes.  The matrix cores do four times the work needed,
-// still under the time of the loads.  The tokens sit in LDS, rows 16 bytes off
-// a multiple of 256 apart, so 16 lanes' reads fall on different banks.
+// still under the time of the loads.  Several tokens sit in LDS, rows 16 bytes
+// off a multiple of 256 apart, so 16 lanes' reads fall on different banks; one
+// token (kOne) is loaded with the weights, as the 16 lanes of a quarter wave
+// then touch four lines, and staging it cost 1.3 us of 8.7 (x [8192, 8192]).
 //
 // The waves of a workgroup take the steps of k in turn, kDepth of them
 // in flight; sums are added through LDS in a fixed order.
@@ -91,7 +93,7 @@ constexpr int64_t kFewLds = 72 << 10;  // two workgroups per CU at the least
 
 __host__ __device__ inline int64_t few_pitch(int64_t k) { return (k + 511) / 512 * 512 + 8; }
 
-template <bool kNV, int RS, int kWaves, int kDepth>
+template <bool kNV, bool kOne, int RS, int kWaves, int kDepth>
 __device__ __forceinline__ void few_body(const MatvecArgs &a, uint16_t *xs)
 {
     constexpr int kGroup = kNV ? 16 : 32, kSb = 32 / kGroup;  // scale bytes per lane and step
@@ -110,8 +112,12 @@ __device__ __forceinline__ void few_body(const MatvecArgs &a, uint16_t *xs)
         sr[i] = a.s + r * (a.k / kGroup) + piece * kSb;
     }
     const float gs = kNV ? *a.g : 1.0f;
-    struct Step { uint32_t w[RS][4], s[RS]; } ring[kDepth];
+    struct Step { uint32_t w[RS][4], s[RS]; uint4 x[kOne ? 4 : 1]; } ring[kDepth];
     auto load = [&](Step &t, int st) {
+        if constexpr (kOne) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) t.x[j] = ld16<false>(a.x + st * 512 + piece * 32 + 8 * j);
+        }
 #pragma unroll
         for (int i = 0; i < RS; ++i) {
             const Words<4> v = *reinterpret_cast<const Words<4> *>(qr[i] + (int64_t)st * 256);
@@ -131,23 +137,25 @@ __device__ __forceinline__ void few_body(const MatvecArgs &a, uint16_t *xs)
         for (int u = 0; u < kDepth; ++u) load(ring[u], min(wave + u * kWaves, full - 1));
     }
 
-    const int pitch = (int)few_pitch(k), width = steps * 64;  // 16-byte pieces of a row, padding included
-    for (int base = threadIdx.x; base < tokens * width; base += kWaves * kWave * 4) {
-        uint4 v[4];
+    const uint16_t *xl = xs + min(row, tokens - 1) * (int)few_pitch(k) + piece * 32;
+    if constexpr (!kOne) {
+        const int pitch = (int)few_pitch(k), width = steps * 64;  // 16-byte pieces of a row, padding included
+        for (int base = threadIdx.x; base < tokens * width; base += kWaves * kWave * 4) {
+            uint4 v[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int e = base + u * kWaves * kWave, t = e / width, c = (e - t * width) * 8;
-            v[u] = make_uint4(0, 0, 0, 0);
-            if (t < tokens && c < k) v[u] = ld16<false>(a.x + t * a.ldx + c);
-        }
+            for (int u = 0; u < 4; ++u) {
+                const int e = base + u * kWaves * kWave, t = e / width, c = (e - t * width) * 8;
+                v[u] = make_uint4(0, 0, 0, 0);
+                if (t < tokens && c < k) v[u] = ld16<false>(a.x + t * a.ldx + c);
+            }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int e = base + u * kWaves * kWave, t = e / width, c = (e - t * width) * 8;
-            if (t < tokens) *reinterpret_cast<uint4 *>(xs + t * pitch + c) = v[u];
+            for (int u = 0; u < 4; ++u) {
+                const int e = base + u * kWaves * kWave, t = e / width, c = (e - t * width) * 8;
+                if (t < tokens) *reinterpret_cast<uint4 *>(xs + t * pitch + c) = v[u];
+            }
         }
+        __syncthreads();
     }
-    const uint16_t *xl = xs + min(row, tokens - 1) * pitch + piece * 32;
-    __syncthreads();
 
     f32x4 acc[RS];
 #pragma unroll
@@ -155,7 +163,9 @@ __device__ __forceinline__ void few_body(const MatvecArgs &a, uint16_t *xs)
     auto multiply = [&](const Step &t, int st) {
         static_for<0, 4, 1>([&](auto J) {
             constexpr int j = J;
-            const bf16x8 b = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(xl + st * 512 + 8 * j));
+            bf16x8 b;
+            if constexpr (kOne) b = __builtin_bit_cast(bf16x8, t.x[j]);
+            else b = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(xl + st * 512 + 8 * j));
 #pragma unroll
             for (int i = 0; i < RS; ++i)
                 acc[i] = mfma(weights8<kNV, j / 2>(t.w[i][j], kNV ? t.s[i] : t.s[i] << 23), b, acc[i]);
@@ -173,6 +183,13 @@ __device__ __forceinline__ void few_body(const MatvecArgs &a, uint16_t *xs)
     if (full < steps && wave == full % kWaves) {  // a partial step: what lies past k counts as zero
         const int valid = k - full * 512 - piece * 32;
         Step &t = ring[0];
+        if constexpr (kOne) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                t.x[j] = make_uint4(0, 0, 0, 0);
+                if (8 * j < valid) t.x[j] = ld16<false>(a.x + full * 512 + piece * 32 + 8 * j);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < RS; ++i) {
             t.s[i] = 0;
@@ -207,11 +224,11 @@ __device__ __forceinline__ void few_body(const MatvecArgs &a, uint16_t *xs)
     }
 }
 
-template <bool kNV, int RS, int kWaves, int kDepth>
+template <bool kNV, bool kOne, int RS, int kWaves, int kDepth>
 __global__ __launch_bounds__(kWaves * 64) void matvec_few_kernel(MatvecArgs a)
 {
     extern __shared__ __align__(16) uint16_t few_xs[];
-    few_body<kNV, RS, kWaves, kDepth>(a, few_xs);
+    few_body<kNV, kOne, RS, kWaves, kDepth>(a, few_xs);
 }
 
 // ---------------------------------------------------------------------------
@@ -411,13 +428,13 @@ __global__ __launch_bounds__(kWaves * 64) void matvec_many_kernel(MatvecArgs a)
     many_body<kNV, RT, NT, kWaves, kDepth>(a);
 }
 
-template <bool kNV, int RS, int kWaves, int kDepth>
+template <bool kNV, bool kOne, int RS, int kWaves, int kDepth>
 hipError_t go_few(const MatvecArgs &a, hipStream_t stream)
 {
     const int64_t gx = (a.n + RS * 4 - 1) / (RS * 4);
     if (gx > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((matvec_few_kernel<kNV, RS, kWaves, kDepth>), dim3((unsigned)gx),
-                       dim3(kWaves * kWave), (unsigned)(a.tokens * few_pitch(a.k) * 2), stream, a);
+    hipLaunchKernelGGL((matvec_few_kernel<kNV, kOne, RS, kWaves, kDepth>), dim3((unsigned)gx),
+                       dim3(kWaves * kWave), kOne ? 0u : (unsigned)(a.tokens * few_pitch(a.k) * 2), stream, a);
     return hipGetLastError();
 }
 
@@ -439,10 +456,11 @@ hipError_t pick_tiles(const MatvecArgs &a, hipStream_t stream)
     return go_many<kNV, RT, 4, 8, 2>(a, stream);
 }
 
-// Measured on MI355X (us, weights from the memory-side cache), one token x
-// [8192, 8192] MXFP4: 8.7 with 8 rows a workgroup and 8 waves, 10.2 with 16
-// rows and 4 waves; four tokens x [8192, 7168]: 9.5 with 16 rows, 11.3 with 8
-// (each workgroup stages the tokens anew); 16 rows by matvec_many: 11.8.
+// Measured on MI355X (us, weights from the memory-side cache).  One token x
+// [8192, 8192] MXFP4: 8.1 with 8 rows and 4 waves a workgroup, 8.5 with 8 and 8,
+// 9.5 with 16 and 8, 9.0 through matvec_many; x [16384, 7168]: 12.2, 13.7, 15.4.
+// A plain read of the codes takes 5.8 and 9.1.  Four tokens x [8192, 7168]: 9.5
+// with 16 rows, 11.3 with 8 (each workgroup stages the tokens anew).
 //
 // More tokens: every workgroup reads all tokens, so few rows cost L2 traffic,
 // many leave CUs without work.  The least strips that need no more than one
@@ -452,8 +470,9 @@ hipError_t pick_tiles(const MatvecArgs &a, hipStream_t stream)
 template <bool kNV>
 hipError_t pick(const MatvecArgs &a, hipStream_t stream)
 {
+    if (a.tokens == 1 && a.k <= 1 << 30) return go_few<kNV, true, 2, 4, 4>(a, stream);
     if (a.tokens <= 4 && a.tokens * few_pitch(a.k) * 2 <= kFewLds)
-        return a.tokens == 1 ? go_few<kNV, 2, 8, 2>(a, stream) : go_few<kNV, 4, 8, 2>(a, stream);
+        return go_few<kNV, false, 4, 8, 2>(a, stream);
     constexpr int64_t kCus = 256;
     if (a.n <= 16 * kCus) return pick_tiles<kNV, 1>(a, stream);
     if (a.n <= 32 * kCus) return pick_tiles<kNV, 2>(a, stream);
