@@ -235,12 +235,14 @@ __global__ __launch_bounds__(kWaves * 64) void matvec_few_kernel(MatvecArgs a)
 // More tokens: RT strips of 16 rows by NT tiles of 16 tokens per workgroup,
 // whose waves split k in contiguous runs of chunks of 128.
 //
-// Loads have lane 4 r + p on the p-th 16 bytes of row (or token) r; ds_bpermute
-// then gives lane (m, kg) what lane 4 m + kg loaded.  For tokens that is the
-// operand (k = 32 j + 8 kg .. from the j-th load).  For weights it is piece kg
-// of row m, and a 4 x 4 transposition over kg (four permlane swaps) makes it
-// dword kg of piece j, the same k.  One scale load covers four chunks.  kDepth
-// chunks of weights, one of tokens are in flight.
+// Loads have four neighbouring lanes on the four 16-byte pieces of a row (or
+// token) r, lane 4 r + (p ^ 2 (r / 8)) on piece p; ds_bpermute then gives lane
+// (m, kg) piece kg of row m.  (The exclusive or lets the 32 lanes that pass
+// together read from 32 different lanes modulo 32; without it a third of the
+// LDS cycles were conflicts.)  For tokens that is the operand (k = 32 j + 8 kg ..
+// from the j-th load).  For weights a 4 x 4 transposition over kg (four permlane
+// swaps) makes it dword kg of piece j, the same k.  One scale load covers four
+// chunks.  kDepth chunks of weights, one of tokens are in flight.
 // ---------------------------------------------------------------------------
 
 // w[j] of lane group kg <- w[kg] of lane group j
@@ -271,7 +273,7 @@ __device__ __forceinline__ void many_body(const MatvecArgs &a)
     constexpr int kGroup = kNV ? 16 : 32, SW = kNV ? 2 : 1;  // scale words per row and chunk
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int m = lane & 15, kg = lane >> 4, r4 = lane >> 2, p4 = lane & 3;
+    const int m = lane & 15, kg = lane >> 4, r4 = lane >> 2, p4 = (lane & 3) ^ ((r4 >> 3) << 1);
     const int64_t row0 = (int64_t)blockIdx.x * (RT * 16), tok0 = (int64_t)blockIdx.y * (NT * 16);
     const int64_t n = a.n, k = a.k;
 
@@ -290,7 +292,7 @@ __device__ __forceinline__ void many_body(const MatvecArgs &a)
     const float gs = kNV ? *a.g : 1.0f;
     const int chunks = (int)(k / 128), per = (chunks + kWaves - 1) / kWaves;
     const int c0 = wave * per, c1 = min(chunks, c0 + per), last = chunks - 1;
-    const int from_mk = 4 * (4 * m + kg), from_m = 16 * m;
+    const int flip = (m >> 3) << 1, from_mk = 4 * (4 * m + (kg ^ flip));
 
     f32x4 acc[RT][NT];
 #pragma unroll
@@ -338,7 +340,7 @@ __device__ __forceinline__ void many_body(const MatvecArgs &a)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) w[i][j] = from_lane(from_mk, wb[u % kDepth][i][j]);
 #pragma unroll
-                    for (int j = 0; j < SW; ++j) s[i][j] = from_lane(from_m + 4 * (u & 3), sb[(u / 4) & 1][i][j]);
+                    for (int j = 0; j < SW; ++j) s[i][j] = from_lane(16 * m + 4 * ((u & 3) ^ flip), sb[(u / 4) & 1][i][j]);
                     if constexpr (kNV) {  // bytes 2 j + kg / 2 to bytes 0 and 2
 #pragma unroll
                         for (int j = 0; j < SW; ++j) s[i][j] = kg & 2 ? s[i][j] >> 8 : s[i][j];
