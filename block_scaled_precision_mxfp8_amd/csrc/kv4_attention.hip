@@ -830,6 +830,39 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
 
 constexpr int kMaxSplits = 128;
 
+__device__ __forceinline__ uint2 bf16x4(f32x4 v)
+{
+    return make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
+}
+
+// Joins the splits of many rows: D / 4 lanes a row, four dims a lane.
+template <int D>
+__global__ __launch_bounds__(256) void kv4_join_rows_kernel(const float *__restrict__ part, int64_t lines,
+                                                            int splits, uint16_t *__restrict__ out,
+                                                            float *__restrict__ lse)
+{
+    constexpr int kLanes = D / 4, kRows = 256 / kLanes;
+    const int d = threadIdx.x % kLanes, r = threadIdx.x / kLanes;
+    const int64_t line = (int64_t)blockIdx.x * kRows + r;
+    if (r >= kRows || line >= lines) return;
+    const float2 *ml = reinterpret_cast<const float2 *>(part + splits * lines * D) + line;
+    float top = -INFINITY;
+    for (int s = 0; s < splits; ++s) top = fmaxf(top, ml[s * lines].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    float total = 0.f;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int s = 0; s < splits; ++s) {
+        const float2 v = ml[s * lines];
+        const float f = __builtin_amdgcn_exp2f(v.x - base);
+        total += v.y * f;
+        o += reinterpret_cast<const f32x4 *>(part + (s * lines + line) * D)[d] * f;
+    }
+    o *= total == 0.f ? 0.f : 1.0f / total;
+    reinterpret_cast<uint2 *>(out + line * D)[d] = bf16x4(o);
+    if (lse && d == 0) lse[line] = (top + __builtin_log2f(total)) * kLn2;
+}
+
 // Joins the splits of one row per workgroup: 256 / (D / 4) of them at a time,
 // four dims a thread, then those groups through LDS.
 template <int D>
@@ -868,10 +901,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(const float *__restrict__
 #pragma unroll
     for (int i = 1; i < kGroups; ++i) o += so[i][t];
     o *= total == 0.f ? 0.f : 1.0f / total;
-    const uint2 packed = make_uint2(
-        (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)o[0]) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)o[1]) << 16,
-        (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)o[2]) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)o[3]) << 16);
-    reinterpret_cast<uint2 *>(out + line * D)[t] = packed;
+    reinterpret_cast<uint2 *>(out + line * D)[t] = bf16x4(o);
     if (lse && t == 0) lse[line] = (top + __builtin_log2f(total)) * kLn2;
 }
 
@@ -931,8 +961,15 @@ hipError_t go(const Kv4Attn &a, hipStream_t stream)
                                                           : go_few<D, kFewWaves>(a, gx, gy, stream);
     }
     if (e != hipSuccess || a.splits == 1) return e;
-    hipLaunchKernelGGL((kv4_join_kernel<D>), dim3((unsigned)lines), dim3(256), 0, stream, a.part, lines,
-                       a.splits, a.out, a.lse);
+    // Few rows have their splits joined in parallel, many fill the GPU without
+    // that (32768 rows, two splits: 22 us with a workgroup a row).
+    constexpr int64_t kRows = 256 / (D / 4);
+    if (lines >= 16 * kCus)
+        hipLaunchKernelGGL((kv4_join_rows_kernel<D>), dim3((unsigned)((lines + kRows - 1) / kRows)), dim3(256), 0,
+                           stream, a.part, lines, a.splits, a.out, a.lse);
+    else
+        hipLaunchKernelGGL((kv4_join_kernel<D>), dim3((unsigned)lines), dim3(256), 0, stream, a.part, lines,
+                           a.splits, a.out, a.lse);
     return hipGetLastError();
 }
 

@@ -412,6 +412,20 @@ def test_attention_long_context(gpu):
         attend(gpu, geo, cache, host, q, table, np.array([length], np.int32))
 
 
+@pytest.mark.parametrize("geo", [(2, 64, 16), (4, 96, 48), (2, 128, 64), (2, 192, 32), (2, 256, 16)], ids=str)
+def test_attention_many_rows_split(gpu, geo):
+    """Thousands of rows over split contexts."""
+    heads, dim, page = geo
+    announce(f"attention many rows split {geo}")
+    rng = np.random.default_rng(dim)
+    cache, host = filled_cache(rng, geo, 30)
+    width = -(-2000 // page)
+    table = rng.integers(0, 30, (1, width), dtype=np.int32)
+    tokens = 4100 // (2 * heads)
+    q = to_dev_bf16(bf16_bits(rng.standard_normal((1, tokens, 2 * heads, dim))))
+    attend(gpu, geo, cache, host, q, table, np.array([1900], np.int32))
+
+
 def test_cache_past_32_bits(gpu, orc):
     """Append, attend and copy in pages past 2^31 and 2^32 bytes of a layer."""
     announce("cache past 32 bits")
