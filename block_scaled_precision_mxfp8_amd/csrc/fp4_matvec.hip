@@ -450,25 +450,19 @@ hipError_t go_many(const MatvecArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <bool kNV, int RT>
-hipError_t pick_tiles(const MatvecArgs &a, hipStream_t stream)
-{
-    if (a.tokens <= 16) return go_many<kNV, RT, 1, 8, 2>(a, stream);
-    if (a.tokens <= 32) return go_many<kNV, RT, 2, 8, 2>(a, stream);
-    return go_many<kNV, RT, 4, 8, 2>(a, stream);
-}
-
 // Measured on MI355X (us, weights from the memory-side cache).  One token x
 // [8192, 8192] MXFP4: 8.1 with 8 rows and 4 waves a workgroup, 8.5 with 8 and 8,
 // 9.5 with 16 and 8, 9.0 through matvec_many; x [16384, 7168]: 12.2, 13.7, 15.4.
 // A plain read of the codes takes 5.8 and 9.1.  Four tokens x [8192, 7168]: 9.5
 // with 16 rows, 11.3 with 8 (each workgroup stages the tokens anew).
 //
-// More tokens: every workgroup reads all tokens, so few rows cost L2 traffic,
-// many leave CUs without work.  The least strips that need no more than one
-// workgroup per CU measured best or next to it: 64 tokens x [16384, 7168] 54,
-// 35, 27 with 1, 2, 4 strips; x [4096, 7168] 15.5, 17.3, 22.3; 16 tokens x
-// [8192, 7168] 12.4, 9.7, 11.9; x [2048, 7168] 6.0, 7.2, 10.1.
+// More tokens: small tiles read weights and tokens more often, large ones leave
+// CUs without work.  The smallest that needs no more than one workgroup per CU
+// measured best or next to it.  64 tokens x [512, 7168] take 5.6, 6.7, 9.3,
+// 12.4, 19.7 with (1, 1), (2, 1), (2, 2), (4, 2), (4, 4) strips and tiles of
+// tokens; x [2048, 7168] 11.0, 7.9, 10.4, 14.0, 22.1; x [8192, 7168] 37.5, 26.9,
+// 20.8, 16.2, 23.3; x [16384, 7168] 77, 57, 40, 34, 27.  16 tokens x [4096, 7168]
+// 7.3, 7.9, 11.2 with 1, 2, 4 strips; x [16384, 7168] 21.3, 17.3, 15.7.
 template <bool kNV>
 hipError_t pick(const MatvecArgs &a, hipStream_t stream)
 {
@@ -476,9 +470,16 @@ hipError_t pick(const MatvecArgs &a, hipStream_t stream)
     if (a.tokens <= 4 && a.tokens * few_pitch(a.k) * 2 <= kFewLds)
         return go_few<kNV, false, 4, 8, 2>(a, stream);
     constexpr int64_t kCus = 256;
-    if (a.n <= 16 * kCus) return pick_tiles<kNV, 1>(a, stream);
-    if (a.n <= 32 * kCus) return pick_tiles<kNV, 2>(a, stream);
-    return pick_tiles<kNV, 4>(a, stream);
+    const auto fits = [&](int64_t rt, int64_t nt) {
+        const int64_t y = (a.tokens + nt * 16 - 1) / (nt * 16);
+        return y <= kCus && (a.n + rt * 16 - 1) / (rt * 16) * y <= kCus;
+    };
+    if (fits(1, 1)) return go_many<kNV, 1, 1, 8, 2>(a, stream);
+    if (fits(2, 1)) return go_many<kNV, 2, 1, 8, 2>(a, stream);
+    if (a.tokens <= 16) return go_many<kNV, 4, 1, 8, 2>(a, stream);
+    if (fits(2, 2)) return go_many<kNV, 2, 2, 8, 2>(a, stream);
+    if (a.tokens <= 32 || fits(4, 2)) return go_many<kNV, 4, 2, 8, 2>(a, stream);
+    return go_many<kNV, 4, 4, 8, 2>(a, stream);
 }
 
 }  // namespace

@@ -59,6 +59,20 @@ def test_matvec(gpu, kind, tokens, n, k):
 
 
 @pytest.mark.parametrize("kind", ["mx", "nv"])
+@pytest.mark.parametrize("tokens, n, k", [(15, 8207, 416), (17, 2101, 1184), (33, 4000, 416), (50, 8000, 160),
+                                          (30, 9001, 416), (70, 9001, 1184)])
+def test_matvec_tiles(gpu, kind, tokens, n, k):
+    """Enough rows for each size of tile that a workgroup may take."""
+    announce(f"matvec tiles {kind} {tokens}x{n}x{k}")
+    rng = np.random.default_rng(tokens + n)
+    q, s, g, w = weights(rng, kind, n, k)
+    xb = bf16_bits(rng.standard_normal((tokens, k)))
+    got = product(gpu, kind, to_dev_bf16(xb), q, s, g, torch.float32)
+    want, bound = ref.matvec(ref.bf16_to_f64(xb), w, 1.0 if g is None else float(g))
+    ref.assert_within(kind, got.cpu().numpy(), want, bound)
+
+
+@pytest.mark.parametrize("kind", ["mx", "nv"])
 def test_matvec_strides_and_shapes(gpu, kind):
     """Leading dimensions, padded and misaligned rows, one row of a batch, no rows, no columns."""
     announce(f"matvec strides {kind}")
