@@ -74,34 +74,29 @@ struct MatvecArgs {
 };
 
 // ---------------------------------------------------------------------------
-// Up to 4 tokens: the 16 rows of A are 4 weight rows x 4 slices of k, the 16
-// columns of B 4 tokens x the same 4 slices; of the product only the blocks of
-// equal slices are used, their sum over the slices is the result.  A quad of
-// lanes then reads 64 contiguous bytes of one row and lane (kg, a, p) = (lane
-// / 16, lane / 4 % 4, lane % 4) holds 16 of them, k = 128 kg + 32 p .. of a
-// step of 512: one MXFP4 group, and exactly what four products want, with no
-// exchange between lanes.  The matrix cores do four times the work needed,
-// still under the time of the loads.  Several tokens sit in LDS, rows 16 bytes
-// off a multiple of 256 apart, so 16 lanes' reads fall on different banks; one
-// token (kOne) is loaded with the weights, as the 16 lanes of a quarter wave
-// then touch four lines, and staging it cost 1.3 us of 8.7 (x [8192, 8192]).
+// One token: the 16 rows of A are 4 weight rows x 4 slices of k, column p of B
+// the same slice p of the token (all columns alike modulo 4); of the product
+// only the elements of equal slices are used, their sum over the slices is the
+// result.  A quad of lanes then reads 64 contiguous bytes of one row and lane
+// (kg, row, p) = (lane / 16, lane / 4 % 4, lane % 4) holds 16 of them, k = 128
+// kg + 32 p .. of a step of 512: one MXFP4 group, and exactly what four products
+// want, with no exchange between lanes.  The matrix cores do sixteen times the
+// work needed, still under the time of the loads.  The token is loaded with the
+// weights (16 lanes touch two lines); staging it in LDS cost 1.3 us of 8.7
+// (x [8192, 8192]).
 //
 // The waves of a workgroup take the steps of k in turn, kDepth of them
 // in flight; sums are added through LDS in a fixed order.
 // ---------------------------------------------------------------------------
-constexpr int64_t kFewLds = 72 << 10;  // two workgroups per CU at the least
-
-__host__ __device__ inline int64_t few_pitch(int64_t k) { return (k + 511) / 512 * 512 + 8; }
-
-template <bool kNV, bool kOne, int RS, int kWaves, int kDepth>
-__device__ __forceinline__ void few_body(const MatvecArgs &a, uint16_t *xs)
+template <bool kNV, int RS, int kWaves, int kDepth>
+__device__ __forceinline__ void one_body(const MatvecArgs &a)
 {
     constexpr int kGroup = kNV ? 16 : 32, kSb = 32 / kGroup;  // scale bytes per lane and step
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int kg = lane >> 4, row = (lane >> 2) & 3, p = lane & 3, piece = kg * 4 + p;
     const int64_t row0 = (int64_t)blockIdx.x * (RS * 4);
-    const int tokens = (int)a.tokens, k = (int)a.k;
+    const int k = (int)a.k;
     const int full = k / 512, steps = (k + 511) / 512;
 
     const uint8_t *qr[RS], *sr[RS];
@@ -112,12 +107,10 @@ __device__ __forceinline__ void few_body(const MatvecArgs &a, uint16_t *xs)
         sr[i] = a.s + r * (a.k / kGroup) + piece * kSb;
     }
     const float gs = kNV ? *a.g : 1.0f;
-    struct Step { uint32_t w[RS][4], s[RS]; uint4 x[kOne ? 4 : 1]; } ring[kDepth];
+    struct Step { uint32_t w[RS][4], s[RS]; uint4 x[4]; } ring[kDepth];
     auto load = [&](Step &t, int st) {
-        if constexpr (kOne) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) t.x[j] = ld16<false>(a.x + st * 512 + piece * 32 + 8 * j);
-        }
+        for (int j = 0; j < 4; ++j) t.x[j] = ld16<false>(a.x + st * 512 + piece * 32 + 8 * j);
 #pragma unroll
         for (int i = 0; i < RS; ++i) {
             const Words<4> v = *reinterpret_cast<const Words<4> *>(qr[i] + (int64_t)st * 256);
@@ -137,35 +130,13 @@ __device__ __forceinline__ void few_body(const MatvecArgs &a, uint16_t *xs)
         for (int u = 0; u < kDepth; ++u) load(ring[u], min(wave + u * kWaves, full - 1));
     }
 
-    const uint16_t *xl = xs + min(row, tokens - 1) * (int)few_pitch(k) + piece * 32;
-    if constexpr (!kOne) {
-        const int pitch = (int)few_pitch(k), width = steps * 64;  // 16-byte pieces of a row, padding included
-        for (int base = threadIdx.x; base < tokens * width; base += kWaves * kWave * 4) {
-            uint4 v[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int e = base + u * kWaves * kWave, t = e / width, c = (e - t * width) * 8;
-                v[u] = make_uint4(0, 0, 0, 0);
-                if (t < tokens && c < k) v[u] = ld16<false>(a.x + t * a.ldx + c);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int e = base + u * kWaves * kWave, t = e / width, c = (e - t * width) * 8;
-                if (t < tokens) *reinterpret_cast<uint4 *>(xs + t * pitch + c) = v[u];
-            }
-        }
-        __syncthreads();
-    }
-
     f32x4 acc[RS];
 #pragma unroll
     for (int i = 0; i < RS; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto multiply = [&](const Step &t, int st) {
+    auto multiply = [&](const Step &t) {
         static_for<0, 4, 1>([&](auto J) {
             constexpr int j = J;
-            bf16x8 b;
-            if constexpr (kOne) b = __builtin_bit_cast(bf16x8, t.x[j]);
-            else b = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(xl + st * 512 + 8 * j));
+            const bf16x8 b = __builtin_bit_cast(bf16x8, t.x[j]);
 #pragma unroll
             for (int i = 0; i < RS; ++i)
                 acc[i] = mfma(weights8<kNV, j / 2>(t.w[i][j], kNV ? t.s[i] : t.s[i] << 23), b, acc[i]);
@@ -175,7 +146,7 @@ __device__ __forceinline__ void few_body(const MatvecArgs &a, uint16_t *xs)
         static_for<0, kDepth, 1>([&](auto U) {
             const int st = base + U * kWaves;
             if (st < full) {
-                multiply(ring[U], st);
+                multiply(ring[U]);
                 if (st + kDepth * kWaves < full) load(ring[U], st + kDepth * kWaves);
             }
         });
@@ -183,12 +154,10 @@ __device__ __forceinline__ void few_body(const MatvecArgs &a, uint16_t *xs)
     if (full < steps && wave == full % kWaves) {  // a partial step: what lies past k counts as zero
         const int valid = k - full * 512 - piece * 32;
         Step &t = ring[0];
-        if constexpr (kOne) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                t.x[j] = make_uint4(0, 0, 0, 0);
-                if (8 * j < valid) t.x[j] = ld16<false>(a.x + full * 512 + piece * 32 + 8 * j);
-            }
+        for (int j = 0; j < 4; ++j) {
+            t.x[j] = make_uint4(0, 0, 0, 0);
+            if (8 * j < valid) t.x[j] = ld16<false>(a.x + full * 512 + piece * 32 + 8 * j);
         }
 #pragma unroll
         for (int i = 0; i < RS; ++i) {
@@ -200,35 +169,33 @@ __device__ __forceinline__ void few_body(const MatvecArgs &a, uint16_t *xs)
             for (int j = 0; j < kSb; ++j)
                 if (kGroup * j < valid) t.s[i] |= (uint32_t)sr[i][(int64_t)full * (16 * kSb) + j] << (8 * j);
         }
-        multiply(t, full);
+        multiply(t);
     }
 
-    // lane (kg, t, p) holds rows 4 kg + 0..3 of the product, slices p = 0..3 of
-    // weight row kg, in column (t, p)
-    __shared__ float red[kWaves][RS][16];
+    // lane (kg, any, p) holds rows 4 kg + 0..3 of the product, slices 0..3 of
+    // weight row kg, in a column of slice p
+    __shared__ float red[kWaves][RS][4];
 #pragma unroll
     for (int i = 0; i < RS; ++i) {
         float v = p == 0 ? acc[i][0] : p == 1 ? acc[i][1] : p == 2 ? acc[i][2] : acc[i][3];
         v += __uint_as_float(dpp_swap1(__float_as_uint(v)));
         v += __uint_as_float(dpp_swap2(__float_as_uint(v)));
-        if (p == 0) red[wave][i][lane >> 2] = v;
+        if ((lane & 15) == 0) red[wave][i][kg] = v;
     }
     __syncthreads();
-    if (threadIdx.x < RS * 16) {
-        const int e = threadIdx.x, t = e & 3;
-        const int64_t r = row0 + (e >> 4) * 4 + ((e >> 2) & 3);
-        float v = red[0][e >> 4][e & 15];
+    if (threadIdx.x < RS * 4) {
+        const int i = threadIdx.x >> 2, row_of = threadIdx.x & 3;
+        float v = red[0][i][row_of];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) v += red[w][e >> 4][e & 15];
-        if (t < tokens && r < a.n) store_y(a.y, t * a.ldy + r, v * gs, a.out_f32);
+        for (int w = 1; w < kWaves; ++w) v += red[w][i][row_of];
+        if (row0 + threadIdx.x < a.n) store_y(a.y, row0 + threadIdx.x, v * gs, a.out_f32);
     }
 }
 
-template <bool kNV, bool kOne, int RS, int kWaves, int kDepth>
-__global__ __launch_bounds__(kWaves * 64) void matvec_few_kernel(MatvecArgs a)
+template <bool kNV, int RS, int kWaves, int kDepth>
+__global__ __launch_bounds__(kWaves * 64) void matvec_one_kernel(MatvecArgs a)
 {
-    extern __shared__ __align__(16) uint16_t few_xs[];
-    few_body<kNV, kOne, RS, kWaves, kDepth>(a, few_xs);
+    one_body<kNV, RS, kWaves, kDepth>(a);
 }
 
 // ---------------------------------------------------------------------------
@@ -430,13 +397,13 @@ __global__ __launch_bounds__(kWaves * 64) void matvec_many_kernel(MatvecArgs a)
     many_body<kNV, RT, NT, kWaves, kDepth>(a);
 }
 
-template <bool kNV, bool kOne, int RS, int kWaves, int kDepth>
-hipError_t go_few(const MatvecArgs &a, hipStream_t stream)
+template <bool kNV, int RS, int kWaves, int kDepth>
+hipError_t go_one(const MatvecArgs &a, hipStream_t stream)
 {
     const int64_t gx = (a.n + RS * 4 - 1) / (RS * 4);
     if (gx > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((matvec_few_kernel<kNV, kOne, RS, kWaves, kDepth>), dim3((unsigned)gx),
-                       dim3(kWaves * kWave), kOne ? 0u : (unsigned)(a.tokens * few_pitch(a.k) * 2), stream, a);
+    hipLaunchKernelGGL((matvec_one_kernel<kNV, RS, kWaves, kDepth>), dim3((unsigned)gx),
+                       dim3(kWaves * kWave), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -453,8 +420,9 @@ hipError_t go_many(const MatvecArgs &a, hipStream_t stream)
 // Measured on MI355X (us, weights from the memory-side cache).  One token x
 // [8192, 8192] MXFP4: 8.1 with 8 rows and 4 waves a workgroup, 8.5 with 8 and 8,
 // 9.5 with 16 and 8, 9.0 through matvec_many; x [16384, 7168]: 12.2, 13.7, 15.4.
-// A plain read of the codes takes 5.8 and 9.1.  Four tokens x [8192, 7168]: 9.5
-// with 16 rows, 11.3 with 8 (each workgroup stages the tokens anew).
+// A plain read of the codes takes 5.8 and 9.1.  (With several tokens, staged in
+// LDS, such products took 12.7 for 4 x [8192, 8960] and 4.5 for 2 x [512, 7168],
+// matvec_many 10.3 and 5.5.)
 //
 // More tokens: small tiles read weights and tokens more often, large ones leave
 // CUs without work.  The smallest that needs no more than one workgroup per CU
@@ -466,9 +434,7 @@ hipError_t go_many(const MatvecArgs &a, hipStream_t stream)
 template <bool kNV>
 hipError_t pick(const MatvecArgs &a, hipStream_t stream)
 {
-    if (a.tokens == 1 && a.k <= 1 << 30) return go_few<kNV, true, 2, 4, 4>(a, stream);
-    if (a.tokens <= 4 && a.tokens * few_pitch(a.k) * 2 <= kFewLds)
-        return go_few<kNV, false, 4, 8, 2>(a, stream);
+    if (a.tokens == 1 && a.k <= 1 << 30) return go_one<kNV, 2, 4, 4>(a, stream);
     constexpr int64_t kCus = 256;
     const auto fits = [&](int64_t rt, int64_t nt) {
         const int64_t y = (a.tokens + nt * 16 - 1) / (nt * 16);
