@@ -961,10 +961,12 @@ hipError_t go(const Kv4Attn &a, hipStream_t stream)
                                                           : go_few<D, kFewWaves>(a, gx, gy, stream);
     }
     if (e != hipSuccess || a.splits == 1) return e;
-    // Few rows have their splits joined in parallel, many fill the GPU without
-    // that (32768 rows, two splits: 22 us with a workgroup a row).
+    // Few rows, or many splits, are joined in parallel; many rows fill the GPU
+    // without that.  A workgroup a row and D / 4 lanes a row measured (D = 128)
+    // 22.4 and 8.0 us for 32768 rows of 2 splits, 4.3 and 3.6 for 4096 of 8,
+    // 13.3 and 18.0 for 4096 of 32, 3.6 and 3.6 for 2048 of 4.
     constexpr int64_t kRows = 256 / (D / 4);
-    if (lines >= 16 * kCus)
+    if (lines >= 16 * kCus && a.splits <= 8)
         hipLaunchKernelGGL((kv4_join_rows_kernel<D>), dim3((unsigned)((lines + kRows - 1) / kRows)), dim3(256), 0,
                            stream, a.part, lines, a.splits, a.out, a.lse);
     else
@@ -980,6 +982,8 @@ hipError_t go(const Kv4Attn &a, hipStream_t stream)
 // tiles (2 us each, alone): up to four tiles a wave there is one split, else no
 // less than one tile for a wave (with many rows, eight for the workgroup).
 // Seven sequences that see 1088 tokens: 11 us in one call, 16 with two splits.
+// All workgroups run at once: one more than a CU each costs a second round (seven
+// sequences of 8192, 8 heads of 128: 16.7 us with 4 splits, 24.2 with 5).
 int32_t kv4_attention_splits(int64_t seqs, int64_t tokens, int64_t q_heads, int64_t kv_heads,
                              int64_t dim, int64_t page, int64_t width, int64_t window)
 {
@@ -989,7 +993,7 @@ int32_t kv4_attention_splits(int64_t seqs, int64_t tokens, int64_t q_heads, int6
     const int64_t groups = (rows + tile - 1) / tile * seqs * kv_heads;
     int64_t seen = width * page;
     if (window > 0 && window + tokens + 64 < seen) seen = window + tokens + 64;
-    const int64_t fill = (kCus + groups - 1) / groups;  // a workgroup per CU
+    const int64_t fill = kCus / groups;
     const int64_t tiles = (seen + 63) / 64;
     const int64_t most = many ? tiles / 8 : tiles > 4 * kFewWaves ? tiles / kFewWaves : 1;
     const int64_t s = fill < most ? fill : most;
