@@ -19,7 +19,7 @@
 //     in order.
 //   - The second product contracts over tokens, in two steps of 32; lane kg's
 //     eight operand elements of step s are its tokens 16 kg + 8 s ..: the P
-//     values it already has, rounded to bf16 (relative error 2^-9 each, on
+//     values it already has, rounded to bf16 (relative error 2^-8 at most, on
 //     weights whose sum is taken from the fp32 values).
 //   - V^T's rows are dims, two of which share a byte of 16 neighbouring tokens
 //     (the cache's V layout): one 16-byte load gives a lane both dims for all
@@ -916,11 +916,22 @@ constexpr int64_t kManyGroups = 768;
 // Row tiles of a wave of the many-row kernel.
 constexpr int row_tiles(int dim, int64_t rows) { return dim <= 128 && rows > 128 ? 2 : 1; }
 
-// Rows (query tokens x query heads of one kv head) from which K and V are
-// decoded once for all.
-constexpr int64_t kManyRows = 33;
-
 constexpr int64_t kCus = 256;
+
+// Whether K and V are decoded once for all rows (query tokens x query heads of
+// one kv head) and not for each 16 of them.  That takes 33 rows (49 up to 128
+// dims) to pay, and more workgroups than half the CUs: with fewer, the context
+// is split between them either way, and the few-row kernel's waves, which work
+// alone, split it finer.  8 heads of 128, few rows' kernel and many rows', us:
+// 32 sequences of 4096, 32 rows 51 and 74, 48 rows 66 and 76, 64 rows 87 and 77;
+// one of 8192, 64 rows 14 and 21, 128 rows (64 workgroups) 18 and 27, 512 rows
+// (256) 37 and 47; four of 16384, 128 rows (256) 71 and 62.  Heads of 256: 32
+// sequences of 4096, 32 rows 105 and 114, 36 rows 157 and 116; five of 8192, 48
+// rows (120 workgroups) 47 and 51.
+constexpr bool many_rows(int dim, int64_t rows, int64_t heads)
+{
+    return rows > (dim <= 128 ? 48 : 32) && (rows + 15) / 16 * heads > kCus / 2;
+}
 
 template <int D, int MT>
 hipError_t go_rows(const Kv4Attn &a, int64_t rows, hipStream_t stream)
@@ -953,7 +964,7 @@ hipError_t go(const Kv4Attn &a, hipStream_t stream)
     const int64_t gx = (int64_t)a.seqs * a.geo.heads, lines = (int64_t)a.seqs * a.tokens * a.q_heads;
     if (gx > 0x7FFFFFFF || lines > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
     hipError_t e;
-    if (rows >= kManyRows) {
+    if (many_rows(D, rows, gx)) {
         e = row_tiles(D, rows) == 2 ? go_rows<D, D <= 128 ? 2 : 1>(a, rows, stream) : go_rows<D, 1>(a, rows, stream);
     } else {
         const int64_t gy = (rows + 15) / 16;
@@ -988,7 +999,7 @@ int32_t kv4_attention_splits(int64_t seqs, int64_t tokens, int64_t q_heads, int6
                              int64_t dim, int64_t page, int64_t width, int64_t window)
 {
     const int64_t rows = tokens * (q_heads / kv_heads);
-    const bool many = rows >= kManyRows;
+    const bool many = many_rows((int)dim, rows, seqs * kv_heads);
     const int64_t tile = many ? kShareWaves * row_tiles((int)dim, rows) * 16 : 16;
     const int64_t groups = (rows + tile - 1) / tile * seqs * kv_heads;
     int64_t seen = width * page;

@@ -304,6 +304,25 @@ def test_attention(gpu, geo, tokens, group):
         attend(gpu, geo, cache, host, q, table, lengths, causal=causal, window=window)
 
 
+@pytest.mark.parametrize("geo", GEOS, ids=str)
+@pytest.mark.parametrize("rows", [53, 190])
+def test_attention_many_rows(gpu, geo, rows):
+    """So many rows, in enough workgroups, that they share decoded tiles."""
+    heads, dim, page = geo
+    group = 2 + dim % 3
+    tokens = -(-rows // group)
+    announce(f"attention {geo} rows {tokens * group}")
+    rng = np.random.default_rng(dim * 10 + rows)
+    lengths = np.array([0, 1, tokens - 1, tokens, 15, 16, 17, 63, 64, 65, 333, 700], np.int32)
+    while len(lengths) * heads * (rows // 16) <= 128:
+        lengths = np.concatenate([lengths, rng.integers(0, 200, 7).astype(np.int32)])
+    cache, host = filled_cache(rng, geo, 40)
+    table = rng.integers(0, 40, (len(lengths), -(-700 // page)), dtype=np.int32)
+    q = to_dev_bf16(bf16_bits(rng.standard_normal((len(lengths), tokens, heads * group, dim))))
+    for causal, window in ((True, 0), (False, 0), (True, 29), (False, 100)):
+        attend(gpu, geo, cache, host, q, table, lengths, causal=causal, window=window)
+
+
 @pytest.mark.parametrize("seqs,geo", [(100, (8, 64, 16)), (130, (7, 96, 48)), (100, (8, 128, 32)), (40, (8, 128, 32)), (40, (8, 192, 32)),
                                       (128, (3, 256, 16))], ids=str)
 def test_attention_many_sequences(gpu, seqs, geo):
