@@ -11,14 +11,18 @@
 // long as both operands agree.
 //
 // MXFP4 weights are exact in bf16 and decoded with their scale by one
-// conversion for two.  NVFP4's E2M1 x E4M3 has at most 6 significant bits, also exact in bf16; g
-// multiplies the fp32 sum.
+// conversion for two.  NVFP4's E2M1 x E4M3 has at most 6 significant bits, also
+// exact in bf16; g multiplies the fp32 sum.
 //
 // What limits these kernels is how a wave's loads fall on cache lines: a
 // 16-byte-per-lane load costs about a clock for every line that a group of 16
 // neighbouring lanes touches.  Lane m holding row m, as the matrix cores want
 // it, touches 64 (measured: 72 clocks a load, 37 us for 64 tokens x [16384,
-// 7168]); four neighbouring lanes on 64 bytes of one row touch 16 (27 us).
+// 7168]); four neighbouring lanes on 64 bytes of one row touch 16 (27 us, 25
+// since the lanes of an exchange fall on different LDS banks).  One token is
+// bound by bytes: x [8192, 8192] reads 36 MB in 8 us.  With 64, the loads'
+// address work, the exchanges through LDS, the matrix cores and the decoding
+// take some 8 us each and overlap in part.
 
 #include "fp4_mfma.hpp"
 #include "launch.hpp"

@@ -319,8 +319,16 @@ __device__ __forceinline__ int sequence_of_rank(const Kv4Attn &a, int r)
     return __builtin_amdgcn_readfirstlane(found);
 }
 
-// kWaves waves take the 64-token tiles of one split in turn, each with its own
-// running maximum and sum, and are joined through LDS in a fixed order.
+// Few rows: 16 of one kv head per workgroup, whose kWaves waves take the 64-token
+// tiles of one split in turn, each with its own running maximum and sum, and are
+// joined through LDS in a fixed order.  A wave loads the next tile's codes and
+// scales before it multiplies this one's.
+//
+// Bound by bytes where the cache is large: one query token of 64 sequences of
+// 4096..8192 tokens, 64 query heads on 8 kv heads of 128, reads 418 MB of codes
+// and scales in 71 to 79 us (5.3 to 5.9 TB/s).  A short context is one wave's
+// chain of loads and products: a sequence of 1000 tokens takes 8.5 us, two tiles
+// a wave.
 template <int D, int kWaves, bool kWide>
 __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attention_kernel(Kv4Attn a)
 {
@@ -535,10 +543,11 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attentio
 // codes of the two after it are on their way from memory.  One barrier a tile.
 //
 // Bound by issue: 512 query tokens over 12..16 k cached tokens (2 sequences, 32
-// query heads on 8 kv heads of 128; 234 GFLOP) take 278 us; a tile costs a wave
+// query heads on 8 kv heads of 128; 234 GFLOP) take 254 us; a tile costs a wave
 // some 300 vector and 64 matrix instructions, which the two waves of a SIMD,
 // kept together by the barrier, hardly overlap: the products alone take 135
-// us.  Waves 4..7 half a tile behind the others (two barriers a tile) took 342
+// us.  (Alone; measured like the variants, with the join it had then, 278 us.)
+// Waves 4..7 half a tile behind the others (two barriers a tile) took 342
 // us, MT = 1 328, one tile less in flight 291, no reads ahead of the products
 // in LDS 308; addresses kept in scalar registers, as the few-row kernel has them,
 // 284: fewer instructions, but the waves stay closer together.
