@@ -970,8 +970,9 @@ template <int D>
 hipError_t go(const Kv4Attn &a, hipStream_t stream)
 {
     const int64_t rows = (int64_t)a.tokens * (a.q_heads / a.geo.heads);
-    const int64_t gx = (int64_t)a.seqs * a.geo.heads, lines = (int64_t)a.seqs * a.tokens * a.q_heads;
-    if (gx > 0x7FFFFFFF || lines > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    const int64_t gx = (int64_t)a.seqs * a.geo.heads;
+    if (gx > 0x7FFFFFFF || gx * rows > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    const int64_t lines = gx * rows;
     hipError_t e;
     if (many_rows(D, rows, gx)) {
         e = row_tiles(D, rows) == 2 ? go_rows<D, D <= 128 ? 2 : 1>(a, rows, stream) : go_rows<D, 1>(a, rows, stream);
@@ -1008,6 +1009,8 @@ int32_t kv4_attention_splits(int64_t seqs, int64_t tokens, int64_t q_heads, int6
                              int64_t dim, int64_t page, int64_t width, int64_t window)
 {
     const int64_t rows = tokens * (q_heads / kv_heads);
+    // enough workgroups as it is, whatever the tiles (and no product below overflows)
+    if (seqs * kv_heads > kCus || rows > kCus * 256) return 1;
     const bool many = many_rows((int)dim, rows, seqs * kv_heads);
     const int64_t tile = many ? kShareWaves * row_tiles((int)dim, rows) * 16 : 16;
     const int64_t groups = (rows + tile - 1) / tile * seqs * kv_heads;

@@ -117,6 +117,16 @@ def test_attention_refusals(lib):
     assert size(1, 1, 32, 8, 128, 64, 1024, -1) == 0 and size(1, 1, 32, 8, 128, 64, 1024, 256) == 0
 
 
+def test_attention_workspace_of_vast_sizes(lib):
+    """Counts of workgroups whose product passes 64 bits need no split."""
+    size = lib.mxfp4_kv_attention_workspace_size
+    big = (1 << 31) - 1
+    for args in ((1 << 30, 1 << 30, 4096, 4, 64), (1 << 30, 1 << 30, 1 << 30, 1, 64), (big, big, big, 1, 256), (1, big, big, 1, 128),
+                 (big, 1, 8, 8, 128), (1 << 30, 1 << 30, 1 << 20, 1 << 10, 256)):
+        assert size(*args, 16, big // 16, 0) == 0, args
+        assert size(*args, 16, 4, big) == 0, args
+
+
 def test_copy_refusals(lib):
     def f(c=P16, layers=2, ls=4096, pages=4, ps=1024, nbytes=1024, src=P16, dst=P16, n=2):
         return lib.mxfp4_kv_copy_pages(c, layers, ls, pages, ps, nbytes, src, dst, n, NULL)
