@@ -275,9 +275,11 @@ def mxfp4_kv_copy_pages(cache: torch.Tensor, src: torch.Tensor, dst: torch.Tenso
         raise ValueError("cache must be [layers, pages, page_bytes]")
     if last != 1:
         raise ValueError("a page must be contiguous")
+    # both held until the launch: a copy let go of early gives its memory to the next one
+    src, dst = src.contiguous(), dst.contiguous()
     st = (_mxq._lib or _mxq.load()).mxfp4_kv_copy_pages(
-        cache.data_ptr(), layers, layer_stride, pages, page_stride, nbytes,
-        src.contiguous().data_ptr(), dst.contiguous().data_ptr(), src.shape[0], _stream_of(dev))
+        cache.data_ptr(), layers, layer_stride, pages, page_stride, nbytes, src.data_ptr(),
+        dst.data_ptr(), src.shape[0], _stream_of(dev))
     if st:
         raise _mxq.MXQError("mxfp4_kv_copy_pages", st)
 

@@ -256,3 +256,52 @@ def test_pool_tables_and_refusals():
     assert pool.table(["a", "c"])[0].tolist() == [[0, 1], [0, 2]]
     with pytest.raises(ValueError):
         mxq.KVPagePool(-1)
+
+
+# -- what the binding hands to the library -------------------------------------------
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that the binding's checks take for one on the GPU."""
+    is_cuda = True
+
+
+class Recorder:
+    """In the library's place: keeps each call's arguments and what ``look``
+    saw of the memory behind them while the call ran."""
+
+    def __init__(self, look=lambda name, args: None):
+        self.calls, self.look = [], look
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args, self.look(name, args)))
+            return mxq.MXQ_OK
+        return call
+
+
+def record(monkeypatch, **kw):
+    lib = Recorder(**kw)
+    monkeypatch.setattr(mxq, "_lib", lib)
+    monkeypatch.setattr(mxq.decode, "_stream_of", lambda device: 0)
+    return lib
+
+
+@pytest.mark.parametrize("n", [1, 7, 512])
+@pytest.mark.parametrize("how", ["columns", "even and odd", "reversed pairs", "rows"])
+def test_copy_pages_hands_over_both_index_tensors(monkeypatch, n, how):
+    """src and dst of any stride: both are in memory, each with its own
+    values, while the call runs."""
+    pairs = torch.stack((torch.arange(n), 1000 + torch.arange(n)), 1).int()
+    src, dst = {"columns": (pairs[:, 0], pairs[:, 1]),
+                "even and odd": (pairs.flatten()[0::2], pairs.flatten()[1::2]),
+                "reversed pairs": (pairs.flip(1)[:, 1], pairs.flip(1)[:, 0]),
+                "rows": tuple(pairs.t().contiguous())}[how]
+
+    def look(name, args):
+        return [np.ctypeslib.as_array((ctypes.c_int32 * n).from_address(p)).tolist() for p in args[6:8]]
+
+    lib = record(monkeypatch, look=look)
+    mxq.mxfp4_kv_copy_pages(torch.zeros(1, 2, 64, dtype=torch.uint8).as_subclass(OnGpu), src, dst)
+    (name, args, seen), = lib.calls
+    assert name == "mxfp4_kv_copy_pages" and args[8] == n and args[6] != args[7]
+    assert seen == [list(range(n)), list(range(1000, 1000 + n))]

@@ -517,6 +517,25 @@ def test_copy_pages(gpu, layers, geo):
         assert np.array_equal(u8(one), want[0])
 
 
+@pytest.mark.parametrize("n", [1, 7, 512])
+def test_copy_pages_with_strided_indices(gpu, n):
+    """Index tensors as columns of pairs, as even and odd elements, as one of each."""
+    announce(f"copy pages, strided indices {n}")
+    geo = (1, 64, 16)
+    pages = 2 * n + 3
+    rng = np.random.default_rng(n)
+    host = rng.integers(0, 256, (2, pages, ref.page_bytes(*geo)), dtype=np.uint8)
+    pairs = rng.permutation(pages)[:2 * n].reshape(n, 2).astype(np.int32)
+    dev = torch.from_numpy(pairs).cuda()
+    want = host.copy()
+    want[:, pairs[:, 1]] = host[:, pairs[:, 0]]
+    turned = dev.t().contiguous()
+    for src, dst in ((dev[:, 0], dev[:, 1]), (dev.flatten()[0::2], dev.flatten()[1::2]), (turned[0], dev[:, 1]), (dev[:, 0], turned[1])):
+        cache = torch.from_numpy(host).cuda()
+        gpu.mxfp4_kv_copy_pages(cache, src, dst)
+        assert np.array_equal(u8(cache), want)
+
+
 # -- streams and graphs ----------------------------------------------------------
 
 def test_decode_step_on_a_side_stream_and_in_a_graph(gpu):
