@@ -40,6 +40,16 @@ def _need(t: torch.Tensor, what: str, dtype: torch.dtype, device: torch.device):
         raise ValueError(f"{what} must be on {device}")
 
 
+def _as_bytes(t: torch.Tensor, what: str) -> torch.Tensor:
+    """t as uint8; only types of one byte are codes or scales."""
+    if isinstance(t, torch.Tensor):
+        if t.dtype is torch.uint8:
+            return t
+        if t.dtype.itemsize == 1:
+            return t.view(torch.uint8)
+    raise TypeError(f"{what} must be a tensor of bytes")
+
+
 def _rows16(x: torch.Tensor) -> torch.Tensor:
     """x with a unit last stride and 16-byte aligned rows (a copy if it has none)."""
     *rows, unit = x.stride()
@@ -59,10 +69,7 @@ def _matvec(fn: str, x, q, s, g, group: int, out_dtype, out):
     if not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 or not x.is_cuda:
         _mxq._need_bf16_cuda(x)
     dev = x.device
-    if q.dtype is not torch.uint8:
-        q = q.view(torch.uint8)
-    if s.dtype is not torch.uint8:
-        s = s.view(torch.uint8)
+    q, s = _as_bytes(q, "q"), _as_bytes(s, "scale")
     if q.device != dev or s.device != dev:
         raise ValueError(f"q and scale must be on {dev}")
     if q.dim() != 2 or not q.is_contiguous() or not s.is_contiguous():

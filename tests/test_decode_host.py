@@ -305,3 +305,34 @@ def test_copy_pages_hands_over_both_index_tensors(monkeypatch, n, how):
     (name, args, seen), = lib.calls
     assert name == "mxfp4_kv_copy_pages" and args[8] == n and args[6] != args[7]
     assert seen == [list(range(n)), list(range(1000, 1000 + n))]
+
+
+def on_gpu(*shape, dtype=torch.uint8):
+    return torch.zeros(shape, dtype=dtype).as_subclass(OnGpu)
+
+
+@pytest.mark.parametrize("kind", ["mx", "nv"])
+def test_matvec_takes_codes_and_scales_of_one_byte_only(monkeypatch, kind):
+    """Scales of another quantizer, fp32 [n, k/128], have as many bytes as
+    E8M0 ones, and wider codes likewise; neither may pass for them."""
+    lib = record(monkeypatch)
+    group = 32 if kind == "mx" else 16
+    x = on_gpu(2, 256, dtype=torch.bfloat16)
+    rest = () if kind == "mx" else (on_gpu(1, dtype=torch.float32),)
+    call = mxq.mxfp4_matvec if kind == "mx" else mxq.nvfp4_matvec
+    q, s = on_gpu(4, 128), on_gpu(4, 256 // group)
+    for dtype in (torch.float32, torch.bfloat16, torch.int32, torch.int64):
+        wide = s.view(dtype)
+        assert wide.numel() * wide.element_size() == s.numel()
+        with pytest.raises(TypeError):
+            call(x, q, wide, *rest)
+        with pytest.raises(TypeError):
+            call(x, q.view(dtype), s, *rest)
+    with pytest.raises(TypeError):
+        call(x, None, s, *rest)
+    with pytest.raises(TypeError):
+        call(x, q, [1, 2], *rest)
+    assert not lib.calls
+    call(x, q, s, *rest)
+    call(x, q.view(torch.int8), s.view(torch.float8_e8m0fnu if kind == "mx" else torch.float8_e4m3fn), *rest)
+    assert [c[0] for c in lib.calls] == ["mxfp4_matvec" if kind == "mx" else "nvfp4_matvec"] * 2
