@@ -31,14 +31,16 @@
 // place and not masked; a NaN scale (0xFF) decodes to NaN.
 //
 // Masked tokens count for nothing whatever they hold: their scores are
-// replaced, codes are finite by themselves, and V scales are cleared where no
-// row of the tile sees the token.  Where some rows see a token and others do
-// not, a NaN scale is taken out of the product and put into the rows that see
-// it.
+// replaced, and V scales are cleared where no row of the tile sees the token.
+// Where some rows see a token and others do not, a weight of 0 does not silence
+// a V that is not finite.  There "wild" scales (255, NaN; 253 and 254, which
+// pass bf16's range with large codes) are taken out of the product, and
+// add_wild gives them to the rows that see them after the last tile.
+
+#include <limits.h>
 
 #include "fp4_mfma.hpp"
 #include "kv4.hpp"
-
 
 namespace mxq {
 
@@ -50,11 +52,17 @@ __device__ __forceinline__ uint32_t low_bytes(int n)
     return n <= 0 ? 0u : n >= 4 ? ~0u : (1u << (8 * n)) - 1u;
 }
 
-// 0x80 in every byte of w that is 0xFF (exact as a test of the whole word;
-// a byte above a hit may show as well, so callers look at bytes again).
-__device__ __forceinline__ uint32_t has_ff(uint32_t w)
+// 0xFF in every byte of w that is 253 or more: the low seven bits are then 125
+// or more, and adding 3 carries into bit 7.
+__device__ __forceinline__ uint32_t wild_bytes(uint32_t w)
 {
-    return (~w - 0x01010101u) & w & 0x80808080u;
+    return ((((w & 0x7F7F7F7Fu) + 0x03030303u) & w & 0x80808080u) >> 7) * 0xFFu;
+}
+
+// 0xFF in every byte that is 255, of those that wild_bytes found (253..255).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w, uint32_t wild)
+{
+    return (w & (w >> 1) & wild & 0x01010101u) * 0xFFu;
 }
 
 // Over the four lanes of a column, kg = 0..3 (lanes 16 apart), by swaps of half
@@ -203,6 +211,11 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int i)
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
+__device__ __forceinline__ uint32_t &word(uint4 &v, int i)
+{
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
 // Which tokens rows [row0, row0 + n) of one sequence see: [any_lo, any_hi) by
 // any of them, [all_lo, all_hi) by every one.
 struct Range {
@@ -290,6 +303,87 @@ __device__ __forceinline__ void v_frags(uint32_t c0, uint32_t c1, uint32_t s0, u
     odd = as_bf16x8(o[0], o[1], o[2], o[3]);
 }
 
+// Scale byte m % 4 of a word -> bits 23..30, by rotation.
+__device__ __forceinline__ int scale_rotation(int m) { return (8 * (m & 3) + 9) & 31; }
+
+// q.k of 64 tokens, 16 kg + 0..15 of them in this lane.
+template <int D, bool kWide>
+__device__ __forceinline__ void scores(const KTile<D, kWide> &kt, const bf16x8 (&qf)[D / 32], int m, int kg, float (&x)[16])
+{
+    const int rot = scale_rotation(m);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const uint32_t w0 = word(kt.scales[0], u), s0 = __builtin_amdgcn_alignbit(w0, w0, rot);
+        uint32_t s1 = s0;
+        if constexpr (scale_sets(D) == 2) {
+            const uint32_t w1 = word(kt.scales[1], u);
+            s1 = __builtin_amdgcn_alignbit(w1, w1, rot);
+        }
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)  // dims kg D/4 + 8 j ..: the lane's first or second scale group
+            acc = mfma(fp4_frag(kt.codes[u].w[j], 8 * j + kg * (D / 4) % 32 < 32 ? s0 : s1), qf[j], acc);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[4 * u + r] = acc[r];
+    }
+}
+
+// Adds to one strip of rows what a masked tile's product has left out: tokens of
+// wild V scales, for the rows that see them ([jlo, jhi), c and mx as in the
+// softmax, which is over).  2^8 of the weights times 2^-8 of the values is
+// finite, so that rows that do not see them get 0; NaN goes to the rows that do.
+template <int D>
+__device__ __forceinline__ void add_wild(const Kv4Attn &a, const int32_t *table, int h, int tile, int m, int kg,
+                                         const bf16x8 (&qf)[D / 32], int jlo, int jhi, float c, float mx,
+                                         f32x4 (&oe)[D / 32], f32x4 (&oo)[D / 32])
+{
+    constexpr int NG = D / 32;
+    Place<false> kp, vp;
+    KTile<D, false> kt;
+    VTile<D, false> vt;
+    kt.init(a.geo, h, m, kg);
+    vt.init(a.geo, h, m, kg);
+    kp.start(a, table, a.geo.page >> 4, tile, m >> 2);
+    vp.start(a, table, a.geo.page >> 4, tile, kg);
+    kt.load(a, kp, kg);
+    vt.load(a, vp);
+    float x[16];
+    scores<D, false>(kt, qf, m, kg, x);
+    const int first = tile * 64 + 16 * kg, lo = vt.ok ? jlo - first : 16, hi = jhi - first;
+    const float base = mx == -INFINITY ? 0.f : mx * c;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        x[i] = i >= lo && i < hi ? __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -base)) * 256.f : 0.f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        bool nan_seen = false;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t &v = word(vt.scales[g], w);
+            const uint32_t wild = wild_bytes(v), nan = nan_bytes(v, wild);
+            nan_seen |= (nan & low_bytes(hi - 4 * w) & ~low_bytes(lo - 4 * w)) != 0;
+            word(vt.codes[g], w) &= wild & ~nan;
+            v = (v & wild & ~nan) - (0x08080808u & wild & ~nan);
+        }
+        int any = nan_seen;  // by the row of lane m: all its lanes look at their own tokens
+        any |= __shfl_xor(any, 16, kWave);
+        any |= __shfl_xor(any, 32, kWave);
+        if (any) {
+            oe[g] += f32x4{NAN, NAN, NAN, NAN};
+            oo[g] += f32x4{NAN, NAN, NAN, NAN};
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            bf16x8 e, o;
+            v_frags(word(vt.codes[g], 2 * s), word(vt.codes[g], 2 * s + 1), word(vt.scales[g], 2 * s),
+                    word(vt.scales[g], 2 * s + 1), e, o);
+            const bf16x8 p = weights_frag(x, s);
+            oe[g] = mfma(e, p, oe[g]);
+            oo[g] = mfma(o, p, oo[g]);
+        }
+    }
+}
+
 // Sequences are started longest first when the workgroups do not all fit at
 // once, so that the last to run are short: the sequence of rank `r` by length,
 // ties in order.  For at most kRanked sequences; with more of them there are
@@ -361,7 +455,6 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attentio
     }
     const int32_t *table = a.table + b * a.table_stride;
     const float c = exponent_factor(a.scale);
-    const int rot = (8 * (m & 3) + 9) & 31;  // scale byte m % 4 of a word -> bits 23..30
 
     f32x4 oe[NG], oo[NG];  // even and odd dims
 #pragma unroll
@@ -384,72 +477,46 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attentio
         kp.advance(a, table, step_pages, step_blocks, bpp);
         vp.advance(a, table, step_pages, step_blocks, bpp);
     }
+    auto masked = [&](int t, bool ok) {
+        return t * 64 < see.all_lo || t * 64 + 64 > see.all_hi || wave_any(!ok);
+    };
+    int wild_lo = INT_MAX, wild_hi = -1;  // masked tiles that wild scales were taken out of
     // Each operand's registers are loaded anew as soon as they are used: K of
     // the next tile is in flight during the softmax and the second product, V
     // during the first product, page numbers one tile longer.
     for (; tile < tile_end; tile += kWaves) {
         const bool more = tile + kWaves < tile_end;
         float x[16];  // tokens 16 kg + 0..15 of the tile
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const uint32_t w0 = word(kt.scales[0], u), s0 = __builtin_amdgcn_alignbit(w0, w0, rot);
-            uint32_t s1 = s0;
-            if constexpr (scale_sets(D) == 2) {
-                const uint32_t w1 = word(kt.scales[1], u);
-                s1 = __builtin_amdgcn_alignbit(w1, w1, rot);
-            }
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < NG; ++j)  // dims kg D/4 + 8 j ..: the lane's first or second scale group
-                acc = mfma(fp4_frag(kt.codes[u].w[j], 8 * j + kg * (D / 4) % 32 < 32 ? s0 : s1), qf[j], acc);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[4 * u + r] = acc[r];
-        }
+        scores<D, kWide>(kt, qf, m, kg, x);
         if (more) {
             kt.load(a, kp, kg);
             kp.advance(a, table, step_pages, step_blocks, bpp);
         }
 
         const int first = tile * 64 + 16 * kg;  // the lane's first token
-        if (tile * 64 < see.all_lo || tile * 64 + 64 > see.all_hi || wave_any(!vt.ok)) {
+        if (masked(tile, vt.ok)) {
             const int lo = vt.ok ? jlo - first : 16, hi = jhi - first;
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = i >= lo && i < hi ? x[i] : -INFINITY;
             // V scales of tokens no row sees
             const int alo = vt.ok ? see.any_lo - first : 16, ahi = see.any_hi - first;
-            uint32_t bad = 0;
+            uint32_t hits = 0;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const uint32_t keep = low_bytes(ahi - 4 * w) & ~low_bytes(alo - 4 * w);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    uint32_t &v = w == 0 ? vt.scales[g].x : w == 1 ? vt.scales[g].y : w == 2 ? vt.scales[g].z : vt.scales[g].w;
+                    uint32_t &v = word(vt.scales[g], w);
                     v &= keep;
-                    bad |= has_ff(v);
+                    const uint32_t wild = wild_bytes(v);
+                    v &= ~wild;
+                    word(vt.codes[g], w) &= ~wild;
+                    hits |= wild;
                 }
             }
-            if (wave_any(bad != 0)) {  // a NaN group that only some rows may see
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    bool hit = false;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        uint32_t &v = i / 4 == 0 ? vt.scales[g].x : i / 4 == 1 ? vt.scales[g].y : i / 4 == 2 ? vt.scales[g].z : vt.scales[g].w;
-                        const uint32_t byte = 0xFFu << (8 * (i & 3));
-                        if ((v & byte) == byte) {
-                            v &= ~byte;
-                            // the row of lane m; all its lanes look at their own tokens
-                            hit |= i >= lo && i < hi;
-                        }
-                    }
-                    int any = hit;
-                    any |= __shfl_xor(any, 16, kWave);
-                    any |= __shfl_xor(any, 32, kWave);
-                    if (any) {
-                        oe[g] += f32x4{NAN, NAN, NAN, NAN};
-                        oo[g] += f32x4{NAN, NAN, NAN, NAN};
-                    }
-                }
+            if (wave_any(hits != 0)) {
+                wild_lo = min(wild_lo, tile);
+                wild_hi = tile;
             }
         }
 
@@ -478,6 +545,11 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attentio
             vt.load(a, vp);
             vp.advance(a, table, step_pages, step_blocks, bpp);
         }
+    }
+
+    for (int t = wild_lo; t <= wild_hi; t += kWaves) {
+        vp.start(a, table, bpp, t, kg);
+        if (masked(t, vp.ok(a))) add_wild<D>(a, table, h, t, m, kg, qf, jlo, jhi, c, mx, oe, oo);
     }
 
     // join the waves: lane (m, kg) holds dims 32 g + 8 kg + 0..7 of row m
@@ -561,7 +633,7 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
     constexpr int kVRounds = (2 * NG + kShareWaves - 1) / kShareWaves;
     extern __shared__ __align__(16) uint4 shared_frags[];
     uint4 *const kf = shared_frags, *const vf = kf + 2 * 4 * NG * kWave;  // [buffer][frag][lane]
-    __shared__ uint32_t nan_tokens[2][NG][8];  // of a masked tile: bit i of [g][2 kg + s]: token 16 kg + 8 s + i
+    __shared__ int wild_tiles[2][kShareWaves];  // masked tiles, first and last, that a wave took wild scales out of
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int m = lane & 15, kg = lane >> 4;
@@ -605,7 +677,7 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
     const int32_t *table = a.table + b * a.table_stride;
     const int bpp = a.geo.page >> 4, step_pages = 4 / bpp, step_blocks = 4 - step_pages * bpp;
     const int ku = wave >> 1, kj = (wave & 1) * kHalf, kn = wave & 1 ? NG - kHalf : kHalf;
-    const int rot = (8 * (m & 3) + 9) & 31;
+    const int rot = scale_rotation(m);
     Place<false> kp, vp;  // of the next tile
     struct Share {  // of one tile
         uint32_t kc[kHalf], ks[scale_sets(D)];
@@ -648,6 +720,7 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
     auto masked = [&](int tile, bool ok) {
         return tile * 64 < see.all_lo || tile * 64 + 64 > see.all_hi || wave_any(!ok);
     };
+    int wild_lo = INT_MAX, wild_hi = -1;
     auto decode = [&](Share &sh, int tile, int buf) {
 #pragma unroll
         for (int j = 0; j < kHalf; ++j) {
@@ -662,24 +735,22 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
         const bool mask = masked(tile, sh.v_ok);
 #pragma unroll
         for (int r = 0; r < kVRounds; ++r) {
-            const int unit = wave + kShareWaves * r, g = unit >> 1, s = unit & 1;
+            const int unit = wave + kShareWaves * r, s = unit & 1;
             if (unit < 2 * NG) {
-                if (mask) {  // scales of tokens no row sees, and NaN scales, leave the product
+                if (mask) {  // scales of tokens no row sees, and wild ones, leave the product
                     const int first = tile * 64 + 16 * kg + 8 * s;
                     const int lo = sh.v_ok ? see.any_lo - first : 8, hi = see.any_hi - first;
                     sh.vs[r].x &= low_bytes(hi) & ~low_bytes(lo);
                     sh.vs[r].y &= low_bytes(hi - 4) & ~low_bytes(lo - 4);
-                    uint32_t nan = 0;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        uint32_t &w = i < 4 ? sh.vs[r].x : sh.vs[r].y;
-                        const uint32_t byte = 0xFFu << (8 * (i & 3));
-                        if ((w & byte) == byte) {
-                            w &= ~byte;
-                            nan |= 1u << i;
-                        }
+                    const uint32_t wild0 = wild_bytes(sh.vs[r].x), wild1 = wild_bytes(sh.vs[r].y);
+                    sh.vs[r].x &= ~wild0;
+                    sh.vs[r].y &= ~wild1;
+                    sh.vc[r].x &= ~wild0;
+                    sh.vc[r].y &= ~wild1;
+                    if (wave_any((wild0 | wild1) != 0)) {
+                        wild_lo = min(wild_lo, tile);
+                        wild_hi = tile;
                     }
-                    if (m == 0) nan_tokens[buf][g][2 * kg + s] = nan;
                 }
                 bf16x8 e, o;
                 v_frags(sh.vc[r].x, sh.vc[r].y, sh.vs[r].x, sh.vs[r].y, e, o);
@@ -744,20 +815,6 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
                     const int lo = ok ? jlo[i] - first : 16, hi = jhi[i] - first;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) x[i][e] = e >= lo && e < hi ? x[i][e] : -INFINITY;
-                    // tokens this row sees, as bits; those with a NaN scale spoil the group
-                    const uint32_t seen = lo < 16 && hi > 0 ? ((1u << min(hi, 16)) - 1u) & ~((1u << max(lo, 0)) - 1u) : 0u;
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        const uint32_t nan = nan_tokens[buf][g][2 * kg] | nan_tokens[buf][g][2 * kg + 1] << 8;
-                        if (!wave_any(nan != 0)) continue;
-                        int any = (nan & seen) != 0;
-                        any |= __shfl_xor(any, 16, kWave);
-                        any |= __shfl_xor(any, 32, kWave);
-                        if (any) {
-                            oe[i][g] += f32x4{NAN, NAN, NAN, NAN};
-                            oo[i][g] += f32x4{NAN, NAN, NAN, NAN};
-                        }
-                    }
                 }
             }
             bf16x8 p[MT][2];
@@ -802,6 +859,23 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
     for (int tile = begin; tile < end; tile += 2) {
         step(tile, 0);
         if (tile + 1 < end) step(tile + 1, 1);
+    }
+
+    if (lane == 0) {
+        wild_tiles[0][wave] = wild_lo;
+        wild_tiles[1][wave] = wild_hi;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kShareWaves; ++w) {
+        wild_lo = min(wild_lo, wild_tiles[0][w]);
+        wild_hi = max(wild_hi, wild_tiles[1][w]);
+    }
+    for (int tile = wild_lo; tile <= wild_hi; ++tile) {
+        vp.start(a, table, bpp, tile, kg);
+        if (!masked(tile, vp.ok(a))) continue;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) add_wild<D>(a, table, h, tile, m, kg, qf[i], jlo[i], jhi[i], c, mx[i], oe[i], oo[i]);
     }
 
     // lane (m, kg) holds dims 32 g + 8 kg + 0..7 of row m

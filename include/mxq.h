@@ -539,7 +539,9 @@ mxq_status mxfp4_kv_append(const mxq_kv_cache *cache, const uint16_t *k, int64_t
  * (causal != 0) and j > its own position - window (window > 0).  Tokens of a
  * page index outside 0 .. pages - 1 are not seen by any query.  A query that
  * sees nothing gets zeros and lse = -inf.  What masked places hold, NaN
- * included, does not matter.
+ * included, does not matter.  A visible key or value past bf16's range (scales
+ * of 253 and 254 with large codes, which quantizing never writes) may count as
+ * infinite.
  *   q           [seqs, tokens, q_heads, head_dim] bf16, strides in elements
  *               (multiples of 8), 16-byte aligned
  *   page_table  int32 [seqs, width], row stride table_stride
