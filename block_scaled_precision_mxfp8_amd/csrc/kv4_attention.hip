@@ -19,8 +19,9 @@
 //     in order.
 //   - The second product contracts over tokens, in two steps of 32; lane kg's
 //     eight operand elements of step s are its tokens 16 kg + 8 s ..: the P
-//     values it already has, rounded to bf16 (relative error 2^-8 at most, on
-//     weights whose sum is taken from the fp32 values).
+//     values it already has, as a sum of two bf16 numbers (off by 2^-16 at
+//     most), so there are two products.  One bf16 number would be off by 2^-8,
+//     more than the output's own rounding where values cancel.
 //   - V^T's rows are dims, two of which share a byte of 16 neighbouring tokens
 //     (the cache's V layout): one 16-byte load gives a lane both dims for all
 //     its tokens, v_cvt_scalef32_pk_bf16_fp4 decodes a byte with its token's
@@ -278,11 +279,24 @@ __device__ __forceinline__ float softmax_step(float (&x)[16], float c, float &mx
     return f;
 }
 
-__device__ __forceinline__ bf16x8 weights_frag(const float (&x)[16], int s)
+// Weights of tokens 8 s .. as a sum of two bf16 numbers.  What the second costs,
+// with its products: 64 sequences of 4096..8192 tokens 77 us (73 without), the
+// chunk of 2 x 512 tokens 320 to 332 us (252 to 267).
+struct Weights { bf16x8 hi, lo; };
+
+__device__ __forceinline__ Weights weights_frag(const float (&x)[16], int s)
 {
-    return as_bf16x8(bf16x2_rne(x[8 * s], x[8 * s + 1]), bf16x2_rne(x[8 * s + 2], x[8 * s + 3]),
-                     bf16x2_rne(x[8 * s + 4], x[8 * s + 5]), bf16x2_rne(x[8 * s + 6], x[8 * s + 7]));
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = x[8 * s + 2 * i], b = x[8 * s + 2 * i + 1];
+        hi[i] = bf16x2_rne(a, b);
+        lo[i] = bf16x2_rne(a - bf16lo_to_f32(hi[i]), b - bf16hi_to_f32(hi[i]));
+    }
+    return {as_bf16x8(hi[0], hi[1], hi[2], hi[3]), as_bf16x8(lo[0], lo[1], lo[2], lo[3])};
 }
+
+__device__ __forceinline__ f32x4 weigh(bf16x8 v, const Weights &p, f32x4 acc) { return mfma(v, p.hi, mfma(v, p.lo, acc)); }
 
 // V^T operands of 8 tokens (code and scale words of tokens 0..3 and 4..7) for
 // a lane's even and odd dim.
@@ -377,9 +391,9 @@ __device__ __forceinline__ void add_wild(const Kv4Attn &a, const int32_t *table,
             bf16x8 e, o;
             v_frags(word(vt.codes[g], 2 * s), word(vt.codes[g], 2 * s + 1), word(vt.scales[g], 2 * s),
                     word(vt.scales[g], 2 * s + 1), e, o);
-            const bf16x8 p = weights_frag(x, s);
-            oe[g] = mfma(e, p, oe[g]);
-            oo[g] = mfma(o, p, oo[g]);
+            const Weights p = weights_frag(x, s);
+            oe[g] = weigh(e, p, oe[g]);
+            oo[g] = weigh(o, p, oo[g]);
         }
     }
 }
@@ -531,14 +545,14 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attentio
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const bf16x8 p = weights_frag(x, s);
+            const Weights p = weights_frag(x, s);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 bf16x8 e, o;
                 v_frags(word(vt.codes[g], 2 * s), word(vt.codes[g], 2 * s + 1), word(vt.scales[g], 2 * s),
                         word(vt.scales[g], 2 * s + 1), e, o);
-                oe[g] = mfma(e, p, oe[g]);
-                oo[g] = mfma(o, p, oo[g]);
+                oe[g] = weigh(e, p, oe[g]);
+                oo[g] = weigh(o, p, oo[g]);
             }
         }
         if (more) {
@@ -817,7 +831,7 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
                     for (int e = 0; e < 16; ++e) x[i][e] = e >= lo && e < hi ? x[i][e] : -INFINITY;
                 }
             }
-            bf16x8 p[MT][2];
+            Weights p[MT][2];
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 bool moved;
@@ -848,8 +862,13 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
                     const bf16x8 e = __builtin_bit_cast(bf16x8, vv[g & 1][2 * s]), o = __builtin_bit_cast(bf16x8, vv[g & 1][2 * s + 1]);
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
-                        oe[i][g] = mfma(e, p[i][s], oe[i][g]);
-                        oo[i][g] = mfma(o, p[i][s], oo[i][g]);
+                        oe[i][g] = mfma(e, p[i][s].lo, oe[i][g]);
+                        oo[i][g] = mfma(o, p[i][s].lo, oo[i][g]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        oe[i][g] = mfma(e, p[i][s].hi, oe[i][g]);
+                        oo[i][g] = mfma(o, p[i][s].hi, oo[i][g]);
                     }
                 }
             }

@@ -551,8 +551,9 @@ mxq_status mxfp4_kv_append(const mxq_kv_cache *cache, const uint16_t *k, int64_t
  *               the sum of exp(score) over the visible tokens
  *   workspace   >= mxfp4_kv_attention_workspace_size(...) bytes, 16-byte
  *               aligned, no initial contents needed; may be NULL when that is 0
- * Scores, maxima, sums and accumulators are fp32; softmax weights are rounded
- * to bf16 for the product with V.  Magnitudes below 2^-126 may count as zero.
+ * Scores, maxima, sums and accumulators are fp32; for the product with V a
+ * softmax weight is the sum of two bf16 numbers, off by 2^-16 of its size at
+ * most.  Magnitudes below 2^-126 may count as zero.
  * width * page_size is at most 2^30, and window at most 2^30.
  */
 typedef struct mxq_kv_attention {

@@ -95,3 +95,43 @@ def test_values_past_bf16_where_some_rows_see_them(gpu, geo, tokens, group):
             far[b, :, h * group:(h + 1) * group, 32 * g:32 * g + 32] |= (sees[:, None] & over)[:, None]
         gone = far & ~np.isfinite(got)
         ref.assert_within(f"{causal} {window}", np.where(gone, 0, got), np.where(gone, 0, o), ob)
+
+
+@pytest.mark.parametrize("group", [1, 64])
+@pytest.mark.parametrize("page", [16, 64])
+def test_weights_are_not_rounded_to_bf16(gpu, page, group):
+    """Values of both signs and one magnitude: o is their weights' difference,
+    and an error of the weights stands out.
+
+    Scores are exact (four products of a few bits), so each exponent is off by
+    at most 2^-22 |s| and each weight by twice that, as e^x and the largest
+    score are, plus 2^-20 for exp2.  The product takes a weight as two bf16
+    numbers, off by 2^-8 of 2^-8.  Up to 2 n + 64 additions in fp32:
+    |err| <= (2^-16 + 2^-19 + 8 * 2^-22 max |s| + (2 n + 64) 2^-23) sum p |v| + 2^-8 |o|.
+    Weights rounded to bf16 alone would be off by up to 2^-8 of that sum."""
+    announce(f"weights' precision, page {page}, {group} heads")
+    dim, n, seqs = 64, 24, 140
+    geo = (1, dim, page)
+    rng = np.random.default_rng(page + group)
+    width = -(-n // page)
+    host = np.zeros((seqs * width, ref.page_bytes(*geo)), np.uint8)
+    kc, vc, ks, vs = sections(host, geo)
+    kc[:] = rng.integers(0, 256, kc.shape)
+    vc[:] = 0x22 | rng.integers(0, 2, vc.shape) << 3 | rng.integers(0, 2, vc.shape) << 7  # +-1
+    ks[:] = vs[:] = 127
+    table = np.arange(seqs * width, dtype=np.int32).reshape(seqs, width)
+    x = np.zeros((seqs, 1, group, dim))
+    for _ in range(4):
+        x[..., rng.integers(0, dim)] = rng.integers(-8, 9, x.shape[:-1]) / 8
+    lengths = rng.integers(2, n + 1, seqs).astype(np.int32)
+    got, lse = attend(gpu, geo, torch.from_numpy(host).cuda(), to_dev_bf16(bf16_bits(x)), table, lengths, scale=0.125)
+    worst = 0.0
+    for b in range(seqs):
+        k, v = ref.read_pages(host, geo, table[b])
+        k, v = k[0, :lengths[b]], v[0, :lengths[b]]
+        s = 0.125 * (x[b, 0] @ k.T)
+        p = np.exp(s - s.max(-1, keepdims=True))
+        p /= p.sum(-1, keepdims=True)
+        o = p @ v
+        bound = (2.0 ** -16 + 2.0 ** -19 + 2.0 ** -19 * np.abs(s).max() + (2 * n + 64) * 2.0 ** -23) + 2.0 ** -8 * np.abs(o)
+        ref.assert_within(f"sequence {b}", got[b, 0], o, bound)
