@@ -253,27 +253,37 @@ __device__ __forceinline__ bf16x8 load_q(const uint16_t *p, float scale)
     return as_bf16x8(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
 }
 
+// What a row's scores are taken from in the softmax: its running maximum (of q.k,
+// unscaled), 0 while it has none.  The first product starts at minus that, and
+// so gives the difference: exp(scale s - max) = 2^(c (s - max)) for scores of any
+// size, where c s - (c max, rounded) is off by that rounding, whole powers of two
+// for scores past 2^24, and overflows past 2^31.
+__device__ __forceinline__ float softmax_from(float mx) { return mx == -INFINITY ? 0.f : mx; }
+
 // One step of a row's running softmax over the 16 scores of each of its four
-// lanes: x becomes the weights 2^(c x - c max), the running maximum (unscaled)
-// and this lane's sum move on, and the row's earlier sums want the returned
-// factor when `moved`.
+// lanes, less softmax_from(mx): x becomes the weights, the running maximum and
+// this lane's sum move on, and the row's earlier sums want the returned factor
+// when `moved`.
 __device__ __forceinline__ float softmax_step(float (&x)[16], float c, float &mx, float &sum, bool &moved)
 {
     float top = x[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
-    const float mx_new = fmaxf(mx, max_over_kg(top));
-    const float base = mx_new == -INFINITY ? 0.f : mx_new * c;
+    top = max_over_kg(top);
+    const bool up = top > (mx == -INFINITY ? -INFINITY : 0.f);
     float f = 1.f;
-    moved = wave_any(mx_new > mx);
+    moved = wave_any(up);
     if (moved) {
-        f = __builtin_amdgcn_exp2f(mx * c - base);
+        const float by = up ? top : 0.f;
+        f = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(-by * c);
         sum *= f;
-        mx = mx_new;
+        if (up) mx = softmax_from(mx) + by;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] -= by;
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -base));
+        x[i] = __builtin_amdgcn_exp2f(x[i] * c);
         sum += x[i];
     }
     return f;
@@ -320,9 +330,10 @@ __device__ __forceinline__ void v_frags(uint32_t c0, uint32_t c1, uint32_t s0, u
 // Scale byte m % 4 of a word -> bits 23..30, by rotation.
 __device__ __forceinline__ int scale_rotation(int m) { return (8 * (m & 3) + 9) & 31; }
 
-// q.k of 64 tokens, 16 kg + 0..15 of them in this lane.
+// q.k - from of 64 tokens, 16 kg + 0..15 of them in this lane.
 template <int D, bool kWide>
-__device__ __forceinline__ void scores(const KTile<D, kWide> &kt, const bf16x8 (&qf)[D / 32], int m, int kg, float (&x)[16])
+__device__ __forceinline__ void scores(const KTile<D, kWide> &kt, const bf16x8 (&qf)[D / 32], int m, int kg, float from,
+                                       float (&x)[16])
 {
     const int rot = scale_rotation(m);
 #pragma unroll
@@ -333,7 +344,7 @@ __device__ __forceinline__ void scores(const KTile<D, kWide> &kt, const bf16x8 (
             const uint32_t w1 = word(kt.scales[1], u);
             s1 = __builtin_amdgcn_alignbit(w1, w1, rot);
         }
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        f32x4 acc = {-from, -from, -from, -from};
 #pragma unroll
         for (int j = 0; j < D / 32; ++j)  // dims kg D/4 + 8 j ..: the lane's first or second scale group
             acc = mfma(fp4_frag(kt.codes[u].w[j], 8 * j + kg * (D / 4) % 32 < 32 ? s0 : s1), qf[j], acc);
@@ -362,12 +373,10 @@ __device__ __forceinline__ void add_wild(const Kv4Attn &a, const int32_t *table,
     kt.load(a, kp, kg);
     vt.load(a, vp);
     float x[16];
-    scores<D, false>(kt, qf, m, kg, x);
+    scores<D, false>(kt, qf, m, kg, softmax_from(mx), x);
     const int first = tile * 64 + 16 * kg, lo = vt.ok ? jlo - first : 16, hi = jhi - first;
-    const float base = mx == -INFINITY ? 0.f : mx * c;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        x[i] = i >= lo && i < hi ? __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -base)) * 256.f : 0.f;
+    for (int i = 0; i < 16; ++i) x[i] = i >= lo && i < hi ? __builtin_amdgcn_exp2f(x[i] * c) * 256.f : 0.f;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         bool nan_seen = false;
@@ -501,7 +510,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attentio
     for (; tile < tile_end; tile += kWaves) {
         const bool more = tile + kWaves < tile_end;
         float x[16];  // tokens 16 kg + 0..15 of the tile
-        scores<D, kWide>(kt, qf, m, kg, x);
+        scores<D, kWide>(kt, qf, m, kg, softmax_from(mx), x);
         if (more) {
             kt.load(a, kp, kg);
             kp.advance(a, table, step_pages, step_blocks, bpp);
@@ -795,7 +804,9 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
             load(share[buf ^ 1]);
         }
         if (work) {
-            float x[MT][16];  // tokens 16 kg + 0..15 of the tile
+            float x[MT][16], from[MT];  // tokens 16 kg + 0..15 of the tile
+#pragma unroll
+            for (int i = 0; i < MT; ++i) from[i] = softmax_from(mx[i]);
             uint4 kk[2][NG], vv[2][4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -810,7 +821,7 @@ __global__ __launch_bounds__(kShareWaves * 64) void kv4_attention_rows_kernel(Kv
                 __builtin_amdgcn_sched_barrier(0);
                 f32x4 acc[MT];
 #pragma unroll
-                for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int i = 0; i < MT; ++i) acc[i] = f32x4{-from[i], -from[i], -from[i], -from[i]};
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
                     const bf16x8 f = __builtin_bit_cast(bf16x8, kk[u & 1][j]);

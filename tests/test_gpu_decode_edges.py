@@ -135,3 +135,105 @@ def test_weights_are_not_rounded_to_bf16(gpu, page, group):
         o = p @ v
         bound = (2.0 ** -16 + 2.0 ** -19 + 2.0 ** -19 * np.abs(s).max() + (2 * n + 64) * 2.0 ** -23) + 2.0 ** -8 * np.abs(o)
         ref.assert_within(f"sequence {b}", got[b, 0], o, bound)
+
+
+def as_float32(v):
+    with np.errstate(over="ignore"):
+        return np.asarray(v, np.float64).astype(np.float32)
+
+
+def assert_values(name, got, want):
+    """Equal, NaN and infinities too; magnitudes below 2^-126 may be zero."""
+    small = np.abs(want) < 2.0 ** -126
+    same = (got == want) | (np.isnan(got) & np.isnan(want)) | (small & (got == 0))
+    assert same.all(), f"{name}: {(~same).sum()} of {same.size}, first at {tuple(np.argwhere(~same)[0])}: " \
+                       f"{got[~same][0]!r} for {want[~same][0]!r}"
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("group", [1, 64])
+def test_attention_every_scale_and_code(gpu, dim, page, group):
+    """One visible token, whose V comes back as it is and whose score is the
+    lse; its block's other scales are anything.  Then 64 equal tokens."""
+    announce(f"attention, every scale and code {dim} {page} {group}")
+    rng = np.random.default_rng(dim + page + group)
+    geo = (1, dim, page)
+    full = -(-64 // page)  # pages of 64 tokens
+    host = rng.integers(0, 256, (256 * full, ref.page_bytes(*geo)), dtype=np.uint8)
+    kc, vc, ks, vs = sections(host, geo)
+    first = host.reshape(256, full, -1)[:, 0]  # page of token 0
+    kc1, vc1, ks1, vs1 = sections(first, geo)
+    byte = np.arange(256)
+    for g in range(dim // 32):
+        vs1[:, 0, 0, g, 0] = rng.permutation(256)
+    vs1[:, 0, 0, rng.integers(0, dim // 32), 0] = byte
+    kc1[:, 0, 0] = 0  # one code of K is not zero
+    at = rng.integers(0, dim, 256)
+    code = rng.integers(1, 8, 256)
+    kc1[byte, 0, 0, at // 2] = code << 4 * (at % 2)
+    ks1[:, 0, 0, :, 0] = rng.integers(0, 253, (256, dim // 32))
+    ks1[byte, 0, 0, at // 32, 0] = byte
+    table = np.arange(256 * full, dtype=np.int32).reshape(256, full)
+    q = torch.ones(256, 1, group, dim, dtype=torch.bfloat16, device="cuda")
+    got, lse = attend(gpu, geo, torch.from_numpy(host).cuda(), q, table, np.ones(256, np.int32), scale=1.0)
+    _, v = ref.read_pages(first, geo, range(256))
+    v = v.reshape(256, page, dim)[:, 0]
+    # scores past fp32's range have no weight
+    score = as_float32(ref.LEVELS[code] * ref.e8m0_to_f64(byte))
+    fine = byte < 250
+    wide = np.broadcast_to(score[:, None, None], lse.shape)
+    assert (np.abs(lse[fine] - wide[fine]) <= 2.0 ** -21 * wide[fine] + 2.0 ** -120).all()
+    assert np.isnan(lse[255]).all() and np.isnan(got[255]).all()
+    assert_values("one token", got[fine], np.broadcast_to(as_float32(v)[:, None, None], got.shape)[fine])
+    # the same token 64 times, so that the tile is full
+    for block in (vc, vs):
+        whole = block.reshape(256, full, page // 16, -1, 16)
+        whole[:] = whole[:, :1, :1, :, :1]
+    kc[:], ks[:] = 0, 127
+    got, lse = attend(gpu, geo, torch.from_numpy(host).cuda(), q, table, np.full(256, 64, np.int32), scale=1.0)
+    scale = np.repeat(sections(first, geo)[3][:, 0, 0, :, 0], 32, -1)  # of each dim
+    # 64 values are added before the division: past 2^121 that may overflow
+    fine = np.broadcast_to(((scale < 246) | (scale == 255))[:, None, None], got.shape)
+    want = np.broadcast_to(as_float32(v)[:, None, None], got.shape)
+    assert_values("64 tokens", got[fine], want[fine])
+    assert (np.abs(lse - np.log(64)) < 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("group", [1, 64])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("power", [22, 33, 90, 120])
+def test_vast_scores(gpu, power, page, group, sign):
+    """Scores of +-{0, .. 6} 2^power, exact: the largest share all the weight, o
+    is the mean of their values and lse their score plus log of their number.
+    Each weight is 1 but for exp2, the joins and bf16 (2^-16 and 2^-19 as
+    below 2^-8 |o| of the output), lse off by two roundings and log's."""
+    announce(f"vast scores 2^{power} {page} {group} {sign}")
+    dim, seqs = 64, 140
+    geo = (1, dim, page)
+    rng = np.random.default_rng(power + page + group + sign)
+    width = -(-700 // page)
+    pages = 60
+    host = filled_cache(rng, geo, pages)
+    kc, _, ks, _ = sections(host, geo)
+    kc[:] &= 0x77  # keys without signs
+    ks[:] = 127
+    x = np.zeros((seqs, 1, group, dim))
+    at = rng.integers(0, dim, (seqs, group))
+    x[np.arange(seqs)[:, None], 0, np.arange(group), at] = sign * 2.0 ** (power - 3)
+    table = rng.integers(0, pages, (seqs, width)).astype(np.int32)
+    lengths = rng.integers(1, 701, seqs).astype(np.int32)
+    lengths[:100] = rng.integers(1, 9, 100)
+    got, lse = attend(gpu, geo, torch.from_numpy(host).cuda(), to_dev_bf16(bf16_bits(x)), table, lengths, scale=8.0)
+    for b in range(seqs):
+        k, v = ref.read_pages(host, geo, table[b])
+        k, v = k[0, :lengths[b]], v[0, :lengths[b]]
+        s = sign * k[:, at[b]].T * 2.0 ** power  # [group, tokens]
+        top = s.max(-1, keepdims=True)
+        p = (s == top) / (s == top).sum(-1, keepdims=True)
+        o = p @ v
+        bound = (2.0 ** -15 + (lengths[b] + 64) * 2.0 ** -23) * (p @ np.abs(v)) + 2.0 ** -8 * np.abs(o)
+        ref.assert_within(f"sequence {b}", got[b, 0], o, bound)
+        want = top[:, 0] + np.log((s == top).sum(-1))
+        ref.assert_within(f"lse {b}", lse[b, 0], want, 2.0 ** -21 * np.abs(want) + 2.0 ** -18)
