@@ -239,17 +239,25 @@ __device__ __forceinline__ int context_length(const Kv4Attn &a, int b)
 
 // Scores to base-2 exponents: exp(scale s) = 2^(c s).  A negative scale is
 // carried by q's signs, so that c is positive and the largest score can be
-// found before multiplying; a zero scale becomes one that makes every score 0.
+// found before multiplying.  A zero scale is carried by q as well: 0 times it,
+// which makes q.k 0, or NaN where q is not finite.
 __device__ __forceinline__ float exponent_factor(float scale)
 {
     const float c = __builtin_fabsf(scale) * kLog2e;
-    return c == 0.f ? 0x1p-120f : c;
+    return c == 0.f ? 1.f : c;
+}
+
+// 0 times two bf16 numbers.
+__device__ __forceinline__ uint32_t zero_times(uint32_t w)
+{
+    return ((w & 0x7F80u) == 0x7F80u ? 0x7FC0u : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0x7FC00000u : 0u);
 }
 
 __device__ __forceinline__ bf16x8 load_q(const uint16_t *p, float scale)
 {
     const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
     const uint4 v = ld16<false>(p);
+    if (__builtin_fabsf(scale) * kLog2e == 0.f) return as_bf16x8(zero_times(v.x), zero_times(v.y), zero_times(v.z), zero_times(v.w));
     return as_bf16x8(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
 }
 

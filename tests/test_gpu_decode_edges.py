@@ -237,3 +237,31 @@ def test_vast_scores(gpu, power, page, group, sign):
         ref.assert_within(f"sequence {b}", got[b, 0], o, bound)
         want = top[:, 0] + np.log((s == top).sum(-1))
         ref.assert_within(f"lse {b}", lse[b, 0], want, 2.0 ** -21 * np.abs(want) + 2.0 ** -18)
+
+
+@pytest.mark.parametrize("tokens,group", [(1, 2), (50, 2)])
+@pytest.mark.parametrize("scale", [0.0, -0.0])
+def test_zero_scale_of_vast_products(gpu, tokens, group, scale):
+    """With a scale of zero every score is 0 however large q.k is, and NaN
+    where q or k has no finite product."""
+    announce(f"zero scale {tokens}")
+    geo = (1, 64, 16)
+    rng = np.random.default_rng(tokens)
+    seqs, width = 40, 5
+    host = filled_cache(rng, geo, seqs * width)
+    kc, _, ks, _ = sections(host, geo)
+    ks[:] = rng.integers(120, 161, ks.shape)
+    table = rng.permutation(seqs * width).astype(np.int32).reshape(seqs, width)
+    x = rng.standard_normal((seqs, tokens, group, 64)) * np.exp2(rng.integers(60, 120, (seqs, tokens, group, 1)))
+    q = to_dev_bf16(bf16_bits(x))
+    lengths = rng.integers(tokens, 81, seqs).astype(np.int32)
+    cache = torch.from_numpy(host).cuda()
+    got, lse = attend(gpu, geo, cache, q, table, lengths, scale=scale)
+    want = ref.attention(q.double().cpu().numpy(), host, geo, table, lengths, 0.0, True, 0)
+    ref.assert_within("zero", got, want[0], want[2])
+    ref.assert_within("zero lse", lse, want[1], want[3])
+    q[0, 0, 0, 3], q[1, 0, 1, 5] = float("nan"), float("inf")
+    got, lse = attend(gpu, geo, cache, q, table, lengths, scale=scale)
+    assert np.isnan(got[0, 0, 0]).all() and np.isnan(lse[0, 0, 0]) and np.isnan(got[1, 0, 1]).all() and np.isnan(lse[1, 0, 1])
+    got[0, 0, 0] = got[1, 0, 1] = 0
+    assert np.isfinite(got).all()
