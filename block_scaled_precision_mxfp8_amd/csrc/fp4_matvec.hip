@@ -110,7 +110,7 @@ __device__ __forceinline__ void one_body(const MatvecArgs &a)
         qr[i] = a.q + r * (a.k >> 1) + piece * 16;
         sr[i] = a.s + r * (a.k / kGroup) + piece * kSb;
     }
-    const float gs = kNV ? *a.g : 1.0f;
+    const float gs = kNV && a.k > 0 ? *a.g : 1.0f;  // an empty sum is 0 whatever g is
     struct Step { uint32_t w[RS][4], s[RS]; uint4 x[4]; } ring[kDepth];
     auto load = [&](Step &t, int st) {
 #pragma unroll
@@ -260,7 +260,7 @@ __device__ __forceinline__ void many_body(const MatvecArgs &a)
 #pragma unroll
     for (int i = 0; i < NT; ++i) xr[i] = a.x + min(tok0 + i * 16 + r4, a.tokens - 1) * a.ldx + p4 * 8;
 
-    const float gs = kNV ? *a.g : 1.0f;
+    const float gs = kNV && a.k > 0 ? *a.g : 1.0f;  // an empty sum is 0 whatever g is
     const int chunks = (int)(k / 128), per = (chunks + kWaves - 1) / kWaves;
     const int c0 = wave * per, c1 = min(chunks, c0 + per), last = chunks - 1;
     const int flip = (m >> 3) << 1, from_mk = 4 * (4 * m + (kg ^ flip));

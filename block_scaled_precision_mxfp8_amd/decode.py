@@ -83,7 +83,7 @@ def _matvec(fn: str, x, q, s, g, group: int, out_dtype, out):
         raise ValueError(f"scale must be [{n}, {k}/{group}]")
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError("out_dtype must be bfloat16 or float32")
-    x2 = x if len(shape) == 2 else x.reshape(-1, k)
+    x2 = x if len(shape) == 2 else x.reshape(shape[:-1].numel(), k)
     ldx, unit = x2.stride()
     xp = x2.data_ptr()
     if unit != 1 or ldx % 8 or ldx < k or xp % 16:

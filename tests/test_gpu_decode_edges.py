@@ -265,3 +265,18 @@ def test_zero_scale_of_vast_products(gpu, tokens, group, scale):
     assert np.isnan(got[0, 0, 0]).all() and np.isnan(lse[0, 0, 0]) and np.isnan(got[1, 0, 1]).all() and np.isnan(lse[1, 0, 1])
     got[0, 0, 0] = got[1, 0, 1] = 0
     assert np.isfinite(got).all()
+
+
+@pytest.mark.parametrize("tokens", [1, 5, 70])
+@pytest.mark.parametrize("g", [1.0, float("nan"), float("inf")])
+def test_products_over_no_columns_are_zero(gpu, tokens, g):
+    """An empty sum is 0 whatever the weights' scale is; rows in any shape."""
+    announce(f"no columns {tokens} {g}")
+    x = torch.ones(tokens, 0, dtype=torch.bfloat16, device="cuda")
+    q, s = (torch.zeros(33, 0, dtype=torch.uint8, device="cuda") for _ in range(2))
+    for dtype in (torch.bfloat16, torch.float32):
+        for rows in (x, x.view(tokens, 1, 0), x.view(1, tokens, 0)):
+            out = torch.full((*rows.shape[:-1], 33), 7.0, dtype=dtype, device="cuda")
+            gpu.nvfp4_matvec(rows, q, s, torch.tensor([g], device="cuda"), out_dtype=dtype, out=out)
+            assert not out.any()
+            assert not gpu.mxfp4_matvec(rows, q, s, out_dtype=dtype).any()
