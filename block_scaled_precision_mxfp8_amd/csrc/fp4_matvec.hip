@@ -414,11 +414,21 @@ hipError_t go_one(const MatvecArgs &a, hipStream_t stream)
 template <bool kNV, int RT, int NT, int kWaves, int kDepth>
 hipError_t go_many(const MatvecArgs &a, hipStream_t stream)
 {
-    const int64_t gx = (a.n + RT * 16 - 1) / (RT * 16), gy = (a.tokens + NT * 16 - 1) / (NT * 16);
-    if (gx > 0x7FFFFFFF || gy > 65535) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((matvec_many_kernel<kNV, RT, NT, kWaves, kDepth>),
-                       dim3((unsigned)gx, (unsigned)gy), dim3(kWaves * kWave), 0, stream, a);
-    return hipGetLastError();
+    const int64_t gx = (a.n + RT * 16 - 1) / (RT * 16);
+    if (gx > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    constexpr int64_t kMost = 65535 * NT * 16;  // tokens of one launch
+    for (int64_t t = 0; t < a.tokens; t += kMost) {
+        MatvecArgs part = a;
+        part.x += t * a.ldx;
+        part.y = static_cast<uint8_t *>(a.y) + t * a.ldy * (a.out_f32 ? 4 : 2);
+        part.tokens = a.tokens - t < kMost ? a.tokens - t : kMost;
+        hipLaunchKernelGGL((matvec_many_kernel<kNV, RT, NT, kWaves, kDepth>),
+                           dim3((unsigned)gx, (unsigned)((part.tokens + NT * 16 - 1) / (NT * 16))),
+                           dim3(kWaves * kWave), 0, stream, part);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 // Measured on MI355X (us, weights from the memory-side cache).  One token x

@@ -280,3 +280,29 @@ def test_products_over_no_columns_are_zero(gpu, tokens, g):
             gpu.nvfp4_matvec(rows, q, s, torch.tensor([g], device="cuda"), out_dtype=dtype, out=out)
             assert not out.any()
             assert not gpu.mxfp4_matvec(rows, q, s, out_dtype=dtype).any()
+
+
+@pytest.mark.parametrize("kind", ["mx", "nv"])
+def test_matvec_of_millions_of_tokens(gpu, kind):
+    """More token tiles than one launch holds."""
+    announce(f"matvec of millions of tokens {kind}")
+    tokens, n, k = 65535 * 64 + 77, 3, 32
+    x = torch.randn(tokens, k, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).bfloat16()
+    rng = np.random.default_rng(2)
+    q = rng.integers(0, 256, (n, k // 2), dtype=np.uint8)
+    if kind == "mx":
+        s = rng.integers(124, 130, (n, 1), dtype=np.uint8)
+        w = ref.fp4_values(q) * np.repeat(ref.e8m0_to_f64(s), 32, -1)
+        call = lambda **kw: gpu.mxfp4_matvec(x, torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda(), **kw)  # noqa: E731
+    else:
+        s = rng.integers(0x30, 0x50, (n, 2), dtype=np.uint8)
+        w = ref.fp4_values(q) * np.repeat(ref.e4m3_to_f64(s), 16, -1)
+        call = lambda **kw: gpu.nvfp4_matvec(x, torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda(),  # noqa: E731
+                                             torch.ones(1, device="cuda"), **kw)
+    w = torch.from_numpy(w).cuda()
+    want = torch.mm(x.double(), w.t().contiguous())
+    bound = (k + 16) * 2.0 ** -23 * torch.mm(x.double().abs(), w.abs().t().contiguous()) + 2.0 ** -24 * want.abs()
+    got = call(out_dtype=torch.float32)
+    assert ((got.double() - want).abs() <= bound).all()
+    got = call()
+    assert ((got.double() - want).abs() <= bound + 2.0 ** -8 * want.abs()).all()
