@@ -239,12 +239,13 @@ __device__ __forceinline__ int context_length(const Kv4Attn &a, int b)
 
 // Scores to base-2 exponents: exp(scale s) = 2^(c s).  A negative scale is
 // carried by q's signs, so that c is positive and the largest score can be
-// found before multiplying.  A zero scale is carried by q as well: 0 times it,
-// which makes q.k 0, or NaN where q is not finite.
+// found before multiplying.  Scales of zero and NaN are carried by q as well
+// (times 0, which makes q.k 0 or, where q is not finite, NaN; and NaN), with a c
+// of 1, so that masked scores stay -inf.
 __device__ __forceinline__ float exponent_factor(float scale)
 {
     const float c = __builtin_fabsf(scale) * kLog2e;
-    return c == 0.f ? 1.f : c;
+    return c > 0.f ? c : 1.f;
 }
 
 // 0 times two bf16 numbers.
@@ -257,7 +258,10 @@ __device__ __forceinline__ bf16x8 load_q(const uint16_t *p, float scale)
 {
     const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
     const uint4 v = ld16<false>(p);
-    if (__builtin_fabsf(scale) * kLog2e == 0.f) return as_bf16x8(zero_times(v.x), zero_times(v.y), zero_times(v.z), zero_times(v.w));
+    if (!(__builtin_fabsf(scale) * kLog2e > 0.f)) {
+        const uint32_t nan = scale != scale ? 0x7FC07FC0u : 0u;
+        return as_bf16x8(zero_times(v.x) | nan, zero_times(v.y) | nan, zero_times(v.z) | nan, zero_times(v.w) | nan);
+    }
     return as_bf16x8(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
 }
 

@@ -306,3 +306,26 @@ def test_matvec_of_millions_of_tokens(gpu, kind):
     assert ((got.double() - want).abs() <= bound).all()
     got = call()
     assert ((got.double() - want).abs() <= bound + 2.0 ** -8 * want.abs()).all()
+
+
+@pytest.mark.parametrize("tokens,group", [(1, 2), (50, 2)])
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_scales_that_are_not_finite(gpu, tokens, group, scale):
+    """Queries that see something get NaN; those that see nothing zeros and -inf."""
+    announce(f"scale {scale} {tokens}")
+    geo = (1, 64, 16)
+    rng = np.random.default_rng(tokens)
+    seqs, width = 40, 5
+    host = filled_cache(rng, geo, seqs * width)
+    table = rng.permutation(seqs * width).astype(np.int32).reshape(seqs, width)
+    table[3, :2] = -1
+    lengths = rng.integers(0, 81, seqs).astype(np.int32)
+    lengths[:4] = 0, 1, tokens, 17
+    q = to_dev_bf16(bf16_bits(rng.standard_normal((seqs, tokens, group, 64))))
+    got, lse = attend(gpu, geo, torch.from_numpy(host).cuda(), q, table, lengths, scale=scale)
+    sees = np.zeros((seqs, tokens, group), bool)
+    for b in range(seqs):
+        at = lengths[b] - tokens + np.arange(tokens)
+        sees[b] = (at >= (32 if b == 3 else 0))[:, None]
+    assert np.isnan(got[sees]).all() and np.isnan(lse[sees]).all()
+    assert not got[~sees].any() and (lse[~sees] == -np.inf).all()
