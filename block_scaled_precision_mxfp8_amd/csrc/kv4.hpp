@@ -78,6 +78,9 @@ hipError_t launch_kv4_copy(uint8_t *cache, int64_t layers, int64_t layer_stride,
 int32_t kv4_attention_splits(int64_t seqs, int64_t tokens, int64_t q_heads, int64_t kv_heads,
                              int64_t dim, int64_t page, int64_t width, int64_t window);
 
+// Most rows (query tokens x query heads of one kv head) an attention call takes.
+int64_t kv4_attention_most_rows(int64_t dim);
+
 hipError_t launch_kv4_attention(const Kv4Attn &a, hipStream_t stream);
 
 }  // namespace mxq

@@ -1062,7 +1062,6 @@ template <int D, int MT>
 hipError_t go_rows(const Kv4Attn &a, int64_t rows, hipStream_t stream)
 {
     const int64_t gx = (int64_t)a.seqs * a.geo.heads, gy = (rows + kShareWaves * MT * 16 - 1) / (kShareWaves * MT * 16);
-    if (gx > 0x7FFFFFFF || gy > 65535) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)a.splits), block(kShareWaves * kWave);
     constexpr unsigned lds = 2 * 8 * (D / 32) * kWave * sizeof(uint4);
     hipLaunchKernelGGL((kv4_attention_rows_kernel<D, MT>), grid, block, lds, stream, a);
@@ -1087,7 +1086,6 @@ hipError_t go(const Kv4Attn &a, hipStream_t stream)
 {
     const int64_t rows = (int64_t)a.tokens * (a.q_heads / a.geo.heads);
     const int64_t gx = (int64_t)a.seqs * a.geo.heads;
-    if (gx > 0x7FFFFFFF || gx * rows > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
     const int64_t lines = gx * rows;
     hipError_t e;
     if (many_rows(D, rows, gx)) {
@@ -1137,6 +1135,11 @@ int32_t kv4_attention_splits(int64_t seqs, int64_t tokens, int64_t q_heads, int6
     const int64_t most = many ? tiles / 8 : tiles > 4 * kFewWaves ? tiles / kFewWaves : 1;
     const int64_t s = fill < most ? fill : most;
     return (int32_t)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
+}
+
+int64_t kv4_attention_most_rows(int64_t dim)
+{
+    return 65535 * (int64_t)(kShareWaves * row_tiles((int)dim, INT_MAX) * 16);  // as many strips as a grid's y holds
 }
 
 hipError_t launch_kv4_attention(const Kv4Attn &a, hipStream_t stream)

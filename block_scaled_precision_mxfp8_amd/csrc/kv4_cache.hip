@@ -171,7 +171,6 @@ template <int D, int kTok>
 hipError_t go_append(const AppendArgs &a, hipStream_t stream)
 {
     const int64_t gx = (a.tokens + kTok - 1) / kTok;
-    if (gx > 0x7FFFFFFF || a.geo.heads > 65535) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((kv4_append_kernel<D, kTok>), dim3((unsigned)gx, (unsigned)a.geo.heads), dim3(256), 0,
                        stream, a.geo, a.cache, a.k, a.k_tok, a.k_head, a.v, a.v_tok, a.v_head, a.slots,
                        a.tokens, a.k_fq, a.v_fq);
@@ -211,8 +210,6 @@ hipError_t launch_kv4_copy(uint8_t *cache, int64_t layers, int64_t layer_stride,
                            const int32_t *dst, int64_t n, hipStream_t stream)
 {
     const int64_t pieces = (page_bytes + 4095) / 4096;
-    if (n > 0x7FFFFFFF || pieces > 0x7FFFFFFF / n || layers > 65535)
-        return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(kv4_copy_kernel, dim3((unsigned)(pieces * n), (unsigned)layers), dim3(256), 0,
                        stream, cache, layer_stride, pages, page_stride, page_bytes, src, dst,
                        (unsigned)pieces);

@@ -726,7 +726,7 @@ mxq_status mxfp4_kv_append(const mxq_kv_cache *cache, const uint16_t *k, int64_t
         v_head_stride % 8)
         return MXQ_EALIGN;
     if (!fits(tokens, (int64_t)geo.heads * geo.dim) || !fits(tokens, k_token_stride) ||
-        !fits(tokens, v_token_stride))
+        !fits(tokens, v_token_stride) || geo.heads > 65535 || tokens > ((int64_t)1 << 34))
         return MXQ_ESIZE;
     return from_hip(mxq::launch_kv4_append(geo, cache->data, k, k_token_stride, k_head_stride, v,
                                            v_token_stride, v_head_stride, slots, tokens, k_fq,
@@ -768,7 +768,9 @@ mxq_status mxfp4_kv_attention(const mxq_kv_cache *cache, const mxq_kv_attention 
         return MXQ_EALIGN;
     const int64_t group = args->q_heads / a.geo.heads, most = (int64_t)1 << 30;
     if ((int64_t)args->width * a.geo.page > most || args->window > most ||
-        args->tokens * group > most || !fits(args->seqs, args->q_seq_stride) ||
+        args->tokens * group > mxq::kv4_attention_most_rows(a.geo.dim) ||
+        (int64_t)args->seqs * a.geo.heads > INT32_MAX / (args->tokens * group) ||
+        !fits(args->seqs, args->q_seq_stride) ||
         !fits(args->tokens, args->q_token_stride) || !fits(args->q_heads, args->q_head_stride) ||
         !fits(args->seqs, args->table_stride))
         return MXQ_ESIZE;
@@ -812,7 +814,9 @@ mxq_status mxfp4_kv_copy_pages(uint8_t *cache, int64_t layers, int64_t layer_str
     if (!aligned(cache, 16) || layer_stride % 16 || page_stride % 16 || page_bytes % 16 ||
         !aligned(src, 4) || !aligned(dst, 4))
         return MXQ_EALIGN;
-    if (!fits(pages, page_stride) || !fits(layers, layer_stride)) return MXQ_ESIZE;
+    if (!fits(pages, page_stride) || !fits(layers, layer_stride) || layers > 65535 ||
+        (page_bytes - 1) / 4096 + 1 > INT32_MAX / n)
+        return MXQ_ESIZE;
     return from_hip(mxq::launch_kv4_copy(cache, layers, layer_stride, pages, page_stride,
                                          page_bytes, src, dst, n, as_stream(stream)));
 }

@@ -24,6 +24,8 @@ import block_scaled_precision_mxfp8_amd as _mxq
 _CACHE = struct.Struct("@Pqqiiii")
 _ATTENTION = struct.Struct("@PqqqPqPiiiifiiiPPPN")
 
+_INT32_MAX = (1 << 31) - 1
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -141,6 +143,8 @@ def mxfp4_kv_page_bytes(kv_heads: int, head_dim: int, page_size: int = 64) -> in
     key = (kv_heads, head_dim, page_size)
     n = _page_bytes.get(key)
     if n is None:
+        if not all(0 < v <= _INT32_MAX for v in key):  # the library's int32 would take them modulo 2^32
+            raise ValueError("heads, head_dim and page_size must be positive 32-bit integers")
         n = _mxq.load().mxfp4_kv_page_bytes(kv_heads, head_dim, page_size)
         if n == 0:
             raise ValueError("the cache has head_dim 64, 96, 128, 192 or 256 and page_size a "
@@ -233,8 +237,8 @@ def mxfp4_kv_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.T
         raise ValueError("lengths must be [seqs]")
     if kv_heads < 1 or heads < 1 or heads % kv_heads:
         raise ValueError("q's heads must be a multiple of kv_heads")
-    if window < 0:
-        raise ValueError("window must not be negative")
+    if not 0 <= window <= _INT32_MAX:
+        raise ValueError("window must be a 32-bit integer that is not negative")
     desc = _layer(cache, dev, kv_heads, dim, page_size)
     q = _rows16(q)
     width = table_shape[1]

@@ -521,6 +521,7 @@ size_t mxfp4_kv_page_bytes(int32_t kv_heads, int32_t head_dim, int32_t page_size
  *           tokens of one call must not have the same slot.
  *   k_fq, v_fq  optional [tokens, kv_heads, head_dim] bf16, contiguous, 16-byte
  *           aligned: the values the cache holds for them; both or neither
+ * At most 65535 kv_heads and 2^34 tokens (MXQ_ESIZE otherwise).
  */
 mxq_status mxfp4_kv_append(const mxq_kv_cache *cache, const uint16_t *k, int64_t k_token_stride,
                            int64_t k_head_stride, const uint16_t *v, int64_t v_token_stride,
@@ -554,7 +555,9 @@ mxq_status mxfp4_kv_append(const mxq_kv_cache *cache, const uint16_t *k, int64_t
  * Scores, maxima, sums and accumulators are fp32; for the product with V a
  * softmax weight is the sum of two bf16 numbers, off by 2^-16 of its size at
  * most.  Magnitudes below 2^-126 may count as zero.
- * width * page_size is at most 2^30, and window at most 2^30.
+ * width * page_size is at most 2^30, and window at most 2^30; seqs * tokens *
+ * q_heads is below 2^31 and tokens * q_heads / kv_heads at most 8388480 (MXQ_ESIZE
+ * otherwise).
  */
 typedef struct mxq_kv_attention {
     const uint16_t *q;
@@ -587,6 +590,8 @@ mxq_status mxfp4_kv_attention(const mxq_kv_cache *cache, const mxq_kv_attention 
  *   src, dst  int32 [n] on the device; a pair with an index outside
  *          0 .. pages - 1 is left out.  No page may be in dst twice, nor be in
  *          dst and, in another pair, in src.
+ * At most 65535 layers, and below 2^31 pieces of 4 KiB in n pages (MXQ_ESIZE
+ * otherwise).
  */
 mxq_status mxfp4_kv_copy_pages(uint8_t *cache, int64_t layers, int64_t layer_stride, int64_t pages,
                                int64_t page_stride, int64_t page_bytes, const int32_t *src,

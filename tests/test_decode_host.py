@@ -336,3 +336,42 @@ def test_matvec_takes_codes_and_scales_of_one_byte_only(monkeypatch, kind):
     call(x, q, s, *rest)
     call(x, q.view(torch.int8), s.view(torch.float8_e8m0fnu if kind == "mx" else torch.float8_e4m3fn), *rest)
     assert [c[0] for c in lib.calls] == ["mxfp4_matvec" if kind == "mx" else "nvfp4_matvec"] * 2
+
+
+# -- sizes past what a launch or 32 bits hold ---------------------------------------------
+
+def test_sizes_past_a_launch_are_refused_as_sizes(lib):
+    """As MXQ_ESIZE, before anything is launched."""
+    many = 65536
+    wide = desc(kv_heads=many, head_dim=64, page_size=16, page_stride=mxq.mxfp4_kv_page_bytes(many, 64, 16))
+    assert lib.mxfp4_kv_append(wide, P16, many * 64, 64, P16, many * 64, 64, P16, 1, NULL, NULL, NULL) == mxq.MXQ_ESIZE
+    assert lib.mxfp4_kv_append(desc(), P16, 0, 0, P16, 0, 0, P16, (1 << 34) + 1, NULL, NULL, NULL) == mxq.MXQ_ESIZE
+    for layers, pages, n in ((65536, 4, 1), (1, 4, 1 << 31), (1, 4, 1 << 40)):
+        assert lib.mxfp4_kv_copy_pages(P16, layers, 4096, pages, 1024, 1024, P16, P16, n, NULL) == mxq.MXQ_ESIZE
+    assert lib.mxfp4_kv_copy_pages(P16, 1, 0, 2, 1 << 30, 1 << 30, P16, P16, 1 << 13, NULL) == mxq.MXQ_ESIZE
+
+    def f(dim, **kw):
+        args = dict(q=P16, q_seq_stride=0, q_token_stride=0, q_head_stride=0, page_table=P16, table_stride=1, lengths=P16, seqs=1,
+                    tokens=1, q_heads=1, width=1, scale=0.1, causal=1, out=P16)
+        c = desc(kv_heads=1, head_dim=dim, page_size=16, page_stride=mxq.mxfp4_kv_page_bytes(1, dim, 16))
+        return lib.mxfp4_kv_attention(c, ctypes.byref(mxq.KVAttentionArgs(**{**args, **kw})), NULL)
+
+    assert f(64, tokens=65535 * 256 + 1) == mxq.MXQ_ESIZE and f(192, tokens=65535 * 128 + 1) == mxq.MXQ_ESIZE
+    assert f(64, tokens=1 << 20, q_heads=16) == mxq.MXQ_ESIZE
+    assert f(64, seqs=1 << 30, tokens=2) == mxq.MXQ_ESIZE and f(64, seqs=1 << 16, q_heads=1 << 15) == mxq.MXQ_ESIZE
+    assert f(64, tokens=(1 << 31) - 1, q_heads=(1 << 31) - 1) == mxq.MXQ_ESIZE
+
+
+def test_sizes_past_32_bits_do_not_wrap(monkeypatch):
+    for geo in ((8, 128, (1 << 32) + 64), ((1 << 32) + 8, 128, 64), (8, (1 << 32) + 128, 64), (8, 128, -64), (0, 128, 64)):
+        with pytest.raises(ValueError):
+            mxq.mxfp4_kv_page_bytes(*geo)
+        with pytest.raises(ValueError):
+            mxq.mxfp4_kv_cache(1, 1, *geo, device="cpu")
+    nbytes = mxq.mxfp4_kv_page_bytes(1, 64, 16)
+    lib = record(monkeypatch)
+    for window in (-1, 1 << 31, (1 << 32) + 5):
+        with pytest.raises(ValueError):
+            mxq.mxfp4_kv_attention(on_gpu(1, 1, 2, 64, dtype=torch.bfloat16), on_gpu(4, nbytes), on_gpu(1, 1, dtype=torch.int32),
+                                   on_gpu(1, dtype=torch.int32), 1, 16, window=window)
+    assert not lib.calls
