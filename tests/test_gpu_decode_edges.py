@@ -329,3 +329,74 @@ def test_scales_that_are_not_finite(gpu, tokens, group, scale):
         sees[b] = (at >= (32 if b == 3 else 0))[:, None]
     assert np.isnan(got[sees]).all() and np.isnan(lse[sees]).all()
     assert not got[~sees].any() and (lse[~sees] == -np.inf).all()
+
+
+@pytest.mark.parametrize("kind", ["mx", "nv"])
+@pytest.mark.parametrize("tokens", [1, 3, 64])
+@pytest.mark.parametrize("k", [288, 2336])
+def test_matvec_every_scale_and_code(gpu, kind, tokens, k):
+    """One weight a row that is not zero, with every scale byte and code, at any
+    column and beside any scales: the product with ones is the weight itself."""
+    announce(f"every scale and code {kind} {tokens} {k}")
+    rng = np.random.default_rng(tokens + k)
+    group = 32 if kind == "mx" else 16
+    byte, code = np.repeat(np.arange(256), 16), np.tile(np.arange(16), 256)
+    n = len(byte)
+    at = rng.integers(0, k, n)
+    q = np.zeros((n, k // 2), np.uint8)
+    q[np.arange(n), at // 2] = code << 4 * (at % 2)
+    # beside it anything but NaN
+    s = rng.integers(0, 255, (n, k // group), dtype=np.uint8)
+    s[s % 128 == 127] -= 1
+    s[np.arange(n), at // group] = byte
+    value = ref.e8m0_to_f64(byte) if kind == "mx" else ref.e4m3_to_f64(byte)
+    want = as_float32(ref.LEVELS[code] * value)
+    want = np.where(code % 8 == 0, np.where(np.isnan(value), np.nan, 0), want)
+    x = torch.ones(tokens, k, dtype=torch.bfloat16, device="cuda")
+    dev = [torch.from_numpy(a).cuda() for a in (q, s)]
+    got = gpu.mxfp4_matvec(x, *dev, out_dtype=torch.float32) if kind == "mx" else \
+        gpu.nvfp4_matvec(x, *dev, torch.ones(1, device="cuda"), out_dtype=torch.float32)
+    assert_values(kind, got.cpu().numpy(), np.broadcast_to(want, (tokens, n)))
+
+
+def holes(rng, table, pages):
+    """A tenth of the entries outside the cache."""
+    table = table.copy()
+    table[rng.random(table.shape) < 0.1] = rng.choice([-1, pages, -7])
+    return table
+
+
+@pytest.mark.parametrize("page", [64, 128, 192])
+@pytest.mark.parametrize("dim", [64, 96, 128])
+def test_attention_of_a_large_batch_in_wide_pages(gpu, dim, page):
+    """Enough workgroups for four waves each, pages of a multiple of 64 tokens,
+    contexts of several tiles a wave."""
+    announce(f"large batch, wide pages {dim} {page}")
+    geo = (8, dim, page)
+    rng = np.random.default_rng(dim + page)
+    pages, seqs = 24, 100
+    host = filled_cache(rng, geo, pages)
+    lengths = rng.integers(0, 1200, seqs).astype(np.int32)
+    lengths[:4] = 0, 1, 1200, 1025
+    table = rng.integers(0, pages, (seqs, -(-1200 // page)), dtype=np.int32)
+    q = to_dev_bf16(bf16_bits(rng.standard_normal((seqs, 1, 8, dim))))
+    check(gpu, geo, host, q, table, lengths)
+    check(gpu, geo, host, q, holes(rng, table, pages), lengths, window=500)
+
+
+@pytest.mark.parametrize("page", [64, 192, 320])
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_attention_of_a_small_batch_in_wide_pages(gpu, dim, page):
+    """Eight waves a workgroup, contexts of several tiles a wave, holes and windows."""
+    announce(f"small batch, wide pages {dim} {page}")
+    geo = (2, dim, page)
+    rng = np.random.default_rng(dim + page)
+    pages, seqs = 13, 5
+    host = filled_cache(rng, geo, pages)
+    lengths = np.array([0, 2000, 1537, 64, 1999], np.int32)
+    table = rng.integers(0, pages, (seqs, -(-2000 // page)), dtype=np.int32)
+    for tokens, group in ((1, 3), (9, 2)):
+        q = to_dev_bf16(bf16_bits(rng.standard_normal((seqs, tokens, 2 * group, dim))))
+        check(gpu, geo, host, q, table, lengths)
+        check(gpu, geo, host, q, holes(rng, table, pages), lengths)
+        check(gpu, geo, host, q, holes(rng, table, pages), lengths, causal=False, window=700)
