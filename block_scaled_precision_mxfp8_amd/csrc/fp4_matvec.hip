@@ -18,11 +18,12 @@
 // 16-byte-per-lane load costs about a clock for every line that a group of 16
 // neighbouring lanes touches.  Lane m holding row m, as the matrix cores want
 // it, touches 64 (measured: 72 clocks a load, 37 us for 64 tokens x [16384,
-// 7168]); four neighbouring lanes on 64 bytes of one row touch 16 (27 us, 25
-// since the lanes of an exchange fall on different LDS banks).  One token is
-// bound by bytes: x [8192, 8192] reads 36 MB in 8 us.  With 64, the loads'
-// address work, the exchanges through LDS, the matrix cores and the decoding
-// take some 8 us each and overlap in part.
+// 7168]); four neighbouring lanes on 64 bytes of one row touch 16 (27 us).  One
+// token is bound by bytes: x [8192, 8192] reads 36 MB in 8 us.  With 64, the
+// loads' address work, the exchanges through LDS (every workgroup exchanges all
+// tokens anew), the matrix cores and the decoding take 6 to 9 us each and hardly
+// overlap.  More than 64 are tiles that read and decode the weights again: 1024 x
+// [16384, 7168] take 357 us, NVFP4 405 (240 GFLOP).
 
 #include "fp4_mfma.hpp"
 #include "launch.hpp"
@@ -440,7 +441,9 @@ hipError_t go_many(const MatvecArgs &a, hipStream_t stream)
 //
 // More tokens: small tiles read weights and tokens more often, large ones leave
 // CUs without work.  The smallest that needs no more than one workgroup per CU
-// measured best or next to it.  64 tokens x [512, 7168] take 5.6, 6.7, 9.3,
+// measured best or next to it, though the step to twice the tile leaves half of
+// the CUs idle (5 tokens x [4096, 7168] take 7.2 us, NVFP4 8.2, x [4097, 7168] 8.3
+// and 10.1).  64 tokens x [512, 7168] take 5.6, 6.7, 9.3,
 // 12.4, 19.7 with (1, 1), (2, 1), (2, 2), (4, 2), (4, 4) strips and tiles of
 // tokens; x [2048, 7168] 11.0, 7.9, 10.4, 14.0, 22.1; x [8192, 7168] 37.5, 26.9,
 // 20.8, 16.2, 23.3; x [16384, 7168] 77, 57, 40, 34, 27.  16 tokens x [4096, 7168]

@@ -28,10 +28,10 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
 }
 
 // The two E2M1 codes of byte kByte times 2^(e - 127) as bf16 (exact), e the
-// exponent field of scale_bits, 255 giving NaN.  v_cvt_scalef32_pk_bf16_fp4
-// reads nothing else of its scale operand (checked for every code and
-// exponent with junk in the sign and the fraction), so a scale word need only
-// be shifted into place.
+// exponent field of scale_bits, 255 giving NaN; past bf16's range (253 and 254
+// with large codes) Inf.  v_cvt_scalef32_pk_bf16_fp4 reads nothing else of its
+// scale operand (checked for every code and exponent with junk in the sign and
+// the fraction), so a scale word need only be shifted into place.
 template <int kByte>
 __device__ __forceinline__ uint32_t fp4_pair(uint32_t codes, uint32_t scale_bits)
 {

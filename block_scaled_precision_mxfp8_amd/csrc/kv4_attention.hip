@@ -90,7 +90,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // NG dwords that are read once: 16-byte pieces with the streaming hint where
 // the address allows them (64 sequences of 4096..8192 tokens, 8 heads of 128:
-// 86 us with the hint on K and V codes, 92 without).
+// 89 us with the hint on K and V codes, 94 without).
 template <int NG>
 __device__ __forceinline__ Words<NG> load_once(const uint8_t *p)
 {
@@ -453,11 +453,11 @@ __device__ __forceinline__ int sequence_of_rank(const Kv4Attn &a, int r)
 // joined through LDS in a fixed order.  A wave loads the next tile's codes and
 // scales before it multiplies this one's.
 //
-// Bound by bytes where the cache is large: one query token of 64 sequences of
-// 4096..8192 tokens, 64 query heads on 8 kv heads of 128, reads 418 MB of codes
-// and scales in 71 to 79 us (5.3 to 5.9 TB/s).  A short context is one wave's
-// chain of loads and products: a sequence of 1000 tokens takes 8.5 us, two tiles
-// a wave.
+// Bound by bytes, and nearly as much by vector issue, where the cache is large:
+// one query token of 64 sequences of 4096..8192 tokens, 64 query heads on 8 kv
+// heads of 128, reads 418 MB of codes and scales in 86 us (4.9 TB/s; the median
+// of launches in a row, 79 the least).  A short context is one wave's chain of
+// loads and products: a sequence of 1000 tokens takes 9.5 us, two tiles a wave.
 template <int D, int kWaves, bool kWide>
 __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attention_kernel(Kv4Attn a)
 {
@@ -650,14 +650,16 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 1) void kv4_attentio
 // codes of the two after it are on their way from memory.  One barrier a tile.
 //
 // Bound by issue: 512 query tokens over 12..16 k cached tokens (2 sequences, 32
-// query heads on 8 kv heads of 128; 234 GFLOP) take 254 us; a tile costs a wave
-// some 300 vector and 64 matrix instructions, which the two waves of a SIMD,
-// kept together by the barrier, hardly overlap: the products alone take 135
-// us.  (Alone; measured like the variants, with the join it had then, 278 us.)
-// Waves 4..7 half a tile behind the others (two barriers a tile) took 342
-// us, MT = 1 328, one tile less in flight 291, no reads ahead of the products
-// in LDS 308; addresses kept in scalar registers, as the few-row kernel has them,
-// 284: fewer instructions, but the waves stay closer together.
+// query heads on 8 kv heads of 128; 234 GFLOP, 351 with the second product of
+// the weights) take 327 us.  A tile costs a wave some 400 vector and 96 matrix
+// instructions; most of the vector ones are the softmax's and the weights', of
+// the same wave's chain of scores, softmax and second product, so that they add
+// up to the products rather than run beside them (the matrix cores are busy 46 %
+// of the time).  MT = 1: 376 us, where this takes 332.  Measured with one product
+// for the weights, when this took 278: waves 4..7 half a tile behind the others
+// (two barriers a tile) 342 us, one tile less in flight 291, no reads ahead of
+// the products in LDS 308, addresses kept in scalar registers as the few-row
+// kernel has them 284.
 // ---------------------------------------------------------------------------
 constexpr int kShareWaves = 8;
 
@@ -1033,8 +1035,8 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(const float *__restrict__
 // Waves of a workgroup of the few-row kernel.  Eight finish a sequence sooner
 // and need fewer splits; four (three workgroups a CU up to 128 dims, whose
 // beginnings and ends then overlap) do better once there are that many.  128
-// sequences of 0..4096 tokens, 8 heads of 128: 66 us with eight, 57 with four;
-// 64 of 4096..8192: 79 and 80; 48 of 0..8192: 48 and 71.
+// sequences of 0..4096 tokens, 8 heads of 128: 75 us with eight, 62 with four; 96
+// of 4096..8192: 125 and 115; 64 of them: 87 and 85; 48 of 0..8192: 48 and 61.
 constexpr int kFewWaves = 8;
 constexpr int64_t kManyGroups = 768;
 
@@ -1048,11 +1050,13 @@ constexpr int64_t kCus = 256;
 // dims) to pay, and more workgroups than half the CUs: with fewer, the context
 // is split between them either way, and the few-row kernel's waves, which work
 // alone, split it finer.  8 heads of 128, few rows' kernel and many rows', us:
-// 32 sequences of 4096, 32 rows 51 and 74, 48 rows 66 and 76, 64 rows 87 and 77;
-// one of 8192, 64 rows 14 and 21, 128 rows (64 workgroups) 18 and 27, 512 rows
-// (256) 37 and 47; four of 16384, 128 rows (256) 71 and 62.  Heads of 256: 32
-// sequences of 4096, 32 rows 105 and 114, 36 rows 157 and 116; five of 8192, 48
-// rows (120 workgroups) 47 and 51.
+// 32 sequences of 4096, 32 rows 58 and 86, 48 rows 75 and 86, 64 rows 98 and 86;
+// one of 8192, 64 rows 14 and 21, 128 rows (64 workgroups) 19 and 29, 512 rows
+// (256) 42 and 50; four of 16384, 128 rows (256) 81 and 71.  32 sequences of 4096
+// with heads of 256: 32 rows 113 and 131, 36 rows 170 and 133; of 192: 32 rows 77
+// and 113, 48 rows 114 and 115; of 64: 48 rows 43 and 73, 64 rows 54 and 74, where
+// the rule is early, as it is with 96: 64 rows 77 and 84.  Five of 8192 with heads
+// of 256, 48 rows (120 workgroups): 51 and 58.
 constexpr bool many_rows(int dim, int64_t rows, int64_t heads)
 {
     return rows > (dim <= 128 ? 48 : 32) && (rows + 15) / 16 * heads > kCus / 2;
@@ -1116,9 +1120,9 @@ hipError_t go(const Kv4Attn &a, hipStream_t stream)
 // second launch and the partial sums, in all about the time of three or four
 // tiles (2 us each, alone): up to four tiles a wave there is one split, else no
 // less than one tile for a wave (with many rows, eight for the workgroup).
-// Seven sequences that see 1088 tokens: 11 us in one call, 16 with two splits.
-// All workgroups run at once: one more than a CU each costs a second round (seven
-// sequences of 8192, 8 heads of 128: 16.7 us with 4 splits, 24.2 with 5).
+// Seven sequences that see 1088 tokens: 8.6 us, 9.5 with two splits.  All
+// workgroups run at once: one more than a CU each costs a second round (seven
+// sequences of 8192, 8 heads of 128: 19.3 us with 4 splits, 27.0 with 5).
 int32_t kv4_attention_splits(int64_t seqs, int64_t tokens, int64_t q_heads, int64_t kv_heads,
                              int64_t dim, int64_t page, int64_t width, int64_t window)
 {

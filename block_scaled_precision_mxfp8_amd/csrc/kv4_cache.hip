@@ -18,9 +18,13 @@ namespace {
 // other blocks (both ends of a run, single tokens) are stored byte by byte.
 //
 // Bound by bytes: 16384 tokens of 8 heads x 128 read 67 MB and write 18 MB, in
-// 20.8 us (4.1 TB/s).  With bytes stored one by one throughout they took 46 us,
-// the 16 partial writes of each 16 bytes being what L2 was busy with.  Small
-// calls are one launch and one trip to memory.
+// 23.4 us (3.6 TB/s; the median of launches in a row).  With bytes stored one by
+// one throughout they took 46 us, the 16 partial writes of each 16 bytes being
+// what L2 was busy with.  A workgroup's tokens start at multiples of kTok of the
+// call, blocks at multiples of 16 slots: of a run that does not begin at one, 16
+// of every 64 tokens lie in blocks that two workgroups share and go byte by byte
+// (a run from slot 0 takes 20.3 us, from slot 5 22.3).  Small calls are one
+// launch and one trip to memory.
 template <int D, int kTok>
 __global__ __launch_bounds__(256) void kv4_append_kernel(
     Kv4Geom geo, uint8_t *__restrict__ cache, const uint16_t *__restrict__ kx, int64_t k_tok,
@@ -179,8 +183,8 @@ hipError_t go_append(const AppendArgs &a, hipStream_t stream)
 
 // Tokens of a workgroup: short windows spread a small call over more CUs, long
 // ones have fewer ends of runs.  With 16 and 64, runs over 8 heads of 128: 33
-// tokens 4.3 and 6.8 us, 2048 tokens 6.5 and 7.3, 4096 tokens 11.2 and 8.7, 16384
-// tokens 35.4 and 20.8; single tokens of 2048 pages 12.0 and 13.5.
+// tokens 4.8 and 7.5 us, 2048 tokens 7.5 and 8.1, 4096 tokens 12.6 and 9.6, 16384
+// tokens 37.0 and 23.6; single tokens of 2048 pages 13.0 and 14.7.
 template <int D>
 hipError_t pick_append(const AppendArgs &a, hipStream_t stream)
 {

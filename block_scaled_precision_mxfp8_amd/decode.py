@@ -116,7 +116,8 @@ def mxfp4_matvec(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor,
                  out: torch.Tensor | None = None) -> torch.Tensor:
     """x [..., k] bf16 times the transpose of the MXFP4 weights (q uint8
     [n, k/2], scale uint8 [n, k/32]): [..., n], summed in fp32, bf16 or fp32.
-    Made for up to 64 rows of x, which read the weights once."""
+    Made for few rows of x: they are taken in tiles of 16, 32 or 64 (larger
+    ones for larger n), each of which reads the weights."""
     return _matvec("mxfp4_matvec", x, q, scale, None, _mxq.MX_GROUP, out_dtype, out)
 
 

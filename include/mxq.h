@@ -475,9 +475,11 @@ mxq_status nvfp4_dequantize(const uint8_t *q_packed, const uint8_t *s_e4m3,
  *   y      [tokens, n] bf16, or fp32 when out_fp32 != 0, row stride ldy
  *          elements, aligned to its element
  * Shape: k % 32 == 0 (MXFP4) or k % 16 == 0 (NVFP4); any tokens and n >= 0;
- * k == 0 writes zeros.  Made for up to 64 tokens, which read the weights once;
- * more run in blocks of 64.  NaN and Inf in x, and NaN scales, reach the sums
- * they belong to.  The order of summation depends on the shape alone.
+ * k == 0 writes zeros.  Made for few tokens: they are taken in tiles of 16, 32
+ * or 64 (larger ones for larger n), each of which reads the weights; one token
+ * has a kernel of its own.  NaN and Inf in x, and NaN scales, reach the sums they
+ * belong to.  Weights below 2^-126 may count as zero.  The order of summation
+ * depends on the shape alone.
  */
 mxq_status mxfp4_matvec(const uint16_t *x, int64_t tokens, int64_t ldx, const uint8_t *q,
                         const uint8_t *scale, int64_t n, int64_t k, void *y, int64_t ldy,
