@@ -47,19 +47,15 @@ def check(gpu, geo, host, q, table, lengths, causal=True, window=0):
     ref.assert_within(name + " lse", got[1], want[1], want[3])
 
 
-# (tokens, query heads): one and two strips of 16 rows; rows that share decoded tiles
-@pytest.mark.parametrize("tokens,group", [(5, 2), (20, 1), (50, 2), (150, 2)])
-@pytest.mark.parametrize("geo", [(2, 64, 16), (1, 96, 48), (2, 128, 64), (1, 192, 192), (1, 256, 16)], ids=str)
-def test_values_past_bf16_where_some_rows_see_them(gpu, geo, tokens, group):
+def wild_case(gpu, geo, tokens, group, seqs, context, masks):
     """V scales of 253 and 254: with small codes ordinary values, with large
     ones past bf16's range, where the result may be infinite, NaN or what real
     numbers give.  On tokens that only some rows of a tile see (causal, window)
     they count for those rows alone."""
     heads, dim, page = geo
-    announce(f"values past bf16 {geo} {tokens}x{group}")
+    announce(f"values past bf16 {geo} {tokens}x{group}, {seqs} sequences of {context}")
     rng = np.random.default_rng(dim + tokens)
-    seqs = max(2, -(-130 // heads // -(-tokens * group // 16)))  # enough workgroups to share tiles from 49 rows on
-    width = -(-400 // page)
+    width = -(-context // page)
     host = filled_cache(rng, geo, seqs * width)
     table = rng.permutation(seqs * width).astype(np.int32).reshape(seqs, width)
     lengths = rng.integers(tokens, width * page + 1, seqs).astype(np.int32)
@@ -78,7 +74,7 @@ def test_values_past_bf16_where_some_rows_see_them(gpu, geo, tokens, group):
                 wild.append((b, t, h, g))
     q = to_dev_bf16(bf16_bits(0.5 * rng.standard_normal((seqs, tokens, heads * group, dim))))
     cache = torch.from_numpy(host).cuda()
-    for causal, window in ((True, 0), (True, 3), (True, 40), (False, tokens + 9)):
+    for causal, window in masks:
         got, lse = attend(gpu, geo, cache, q, table, lengths, causal=causal, window=window)
         o, want_lse, ob, lb = ref.attention(q.double().cpu().numpy(), host, geo, table, lengths, dim ** -0.5, causal, window)
         ref.assert_within("lse", lse, want_lse, lb)
@@ -95,6 +91,22 @@ def test_values_past_bf16_where_some_rows_see_them(gpu, geo, tokens, group):
             far[b, :, h * group:(h + 1) * group, 32 * g:32 * g + 32] |= (sees[:, None] & over)[:, None]
         gone = far & ~np.isfinite(got)
         ref.assert_within(f"{causal} {window}", np.where(gone, 0, got), np.where(gone, 0, o), ob)
+
+
+# (tokens, query heads): one and two strips of 16 rows; rows that share decoded tiles
+@pytest.mark.parametrize("tokens,group", [(5, 2), (20, 1), (50, 2), (150, 2)])
+@pytest.mark.parametrize("geo", [(2, 64, 16), (1, 96, 48), (2, 128, 64), (1, 192, 192), (1, 256, 16)], ids=str)
+def test_values_past_bf16_where_some_rows_see_them(gpu, geo, tokens, group):
+    seqs = max(2, -(-130 // geo[0] // -(-tokens * group // 16)))  # enough workgroups to share tiles from 49 rows on
+    wild_case(gpu, geo, tokens, group, seqs, 400, ((True, 0), (True, 3), (True, 40), (False, tokens + 9)))
+
+
+@pytest.mark.parametrize("geo,tokens,seqs,context", [((2, 64, 16), 3, 2, 3000), ((1, 128, 64), 20, 2, 2600), ((2, 64, 64), 150, 4, 1600),
+                                                     ((4, 192, 32), 70, 4, 1100)], ids=str)
+def test_values_past_bf16_in_split_contexts(gpu, geo, tokens, seqs, context):
+    need = gpu.load().mxfp4_kv_attention_workspace_size(seqs, tokens, 2 * geo[0], *geo, -(-context // geo[2]), 0)
+    assert need > 0  # it is split
+    wild_case(gpu, geo, tokens, 2, seqs, context, ((True, 0),))
 
 
 @pytest.mark.parametrize("group", [1, 64])
