@@ -90,6 +90,11 @@ SIGNATURES = {
     "nvfp4_quantize_grouped_plan": (ctypes.c_int, [_vp, _vp, _vp, _sz, _vp]),
     "mxfp4_matvec": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, ctypes.c_int, _vp]),
     "nvfp4_matvec": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, ctypes.c_int, _vp]),
+    "blockfp8_matmul": (ctypes.c_int, [_vp, _vp]),
+    "mxq_matmul": (ctypes.c_int, [_vp, _vp]),
+    "blockfp8_matmul_grouped": (ctypes.c_int, [_vp, _vp]),
+    "mxq_matmul_grouped": (ctypes.c_int, [_vp, _vp]),
+    "mxq_matmul_wgrad": (ctypes.c_int, [_vp, _vp]),
     "mxfp4_kv_page_bytes": (_sz, [_i32, _i32, _i32]),
     "mxfp4_kv_append": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
     "mxfp4_kv_attention_workspace_size": (_sz, [_i32] * 8),
@@ -714,3 +719,10 @@ def quantize_param(name: str, weight: torch.Tensor):
 
 from .decode import (KVPagePool, mxfp4_kv_append, mxfp4_kv_attention, mxfp4_kv_cache,  # noqa: E402
                      mxfp4_kv_copy_pages, mxfp4_kv_page_bytes, mxfp4_matvec, nvfp4_matvec)
+
+# ---------------------------------------------------------------------------
+# 8-bit linear layers
+# ---------------------------------------------------------------------------
+
+from .linear import (blockfp8_matmul, blockfp8_matmul_grouped, mxfp8_matmul,  # noqa: E402
+                     mxfp8_matmul_grouped, mxfp8_matmul_wgrad)

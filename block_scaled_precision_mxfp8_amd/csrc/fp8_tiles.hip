@@ -1,0 +1,476 @@
+// fp8_tiles.hip -- products of many 8-bit tokens with 8-bit weights for gfx950.
+//
+//   y[r, c] = sum_k x[r, k] w[c, k]
+//
+// in block-FP8 (fp32 scales, x: 1 x 128, w: 128 x 128) and in MXFP8 (E8M0, both 1 x
+// 32), dense, with rows grouped by expert, and with the contraction grouped (weight
+// gradients).
+//
+// Matrix cores: v_mfma_f32_32x32x64_f8f6f4, the weights as A, the tokens as B.  Lane
+// (p, h) = (lane % 32, lane / 32) holds of row p of A (of column p of B) the bytes k =
+// 16 h .. 16 h + 15 and 32 + 16 h .., and of the result column p in rows 8 (i / 4) +
+// 4 h + i % 4, i = 0..15: one token, four neighbouring weight rows.
+//   MXFP8: lane (p, h) gives the scale of row p's group 32 h ..; the products are
+//   scaled and summed in the matrix cores.
+//   Block-FP8: 128 k are multiplied unscaled, from zero, and leave with one FMA an
+//   element: acc += p * (sx * sw).  A lane has one token and a wave's weight rows lie in
+//   one tile of 128, so the factor is one number per lane and 32 tokens.
+
+#include "fp8_matmul.hpp"
+#include "launch.hpp"
+
+namespace mxq {
+
+namespace {
+
+constexpr int kStep = 128;  // k of one step: one line of every row
+
+// 64 lanes' 16 bytes at base + voff + soff into LDS at `lds` + 16 * lane, with no
+// register in between.  In assembly because the compiler would have every later read
+// of LDS wait for it; the loop below waits where it has to.  (m0 is set right before
+// its use, and the compiler has none of its own for it here.)
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds,
+                                            uint32_t voff, uint32_t soff)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "memory");
+}
+
+__device__ __forceinline__ i32x8 join(uint4 a, uint4 b)
+{
+    return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+// 16 codes times a power of two (1 or an MXFP8 scale) as bf16: exact wherever bf16 holds the value.
+__device__ __forceinline__ void decode16(bf16x8 (&d)[2], uint4 q, float scale)
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint2 a = mx_dequant4_hw(w[2 * j], scale), b = mx_dequant4_hw(w[2 * j + 1], scale);
+        d[j] = __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, b.x, b.y));
+    }
+}
+
+struct TileGrid {
+    int32_t tm, tn;  // tiles of rows (at most, if grouped) and of columns
+    int32_t sm, sn;  // tiles of a block that one XCD works on at a time
+    int32_t bm;      // such blocks down
+};
+
+// A block of sm x sn tiles, as many as an XCD has CUs, shares its rows and columns
+// in that XCD's L2.  Workgroup i runs on XCD i % 8.
+__device__ __forceinline__ bool tile_of(const TileGrid &g, int32_t &tm, int32_t &tn)
+{
+    const int32_t xcd = blockIdx.x % 8, local = blockIdx.x / 8, each = g.sm * g.sn;
+    const int32_t block = local / each * 8 + xcd, in = local % each;
+    tm = block % g.bm * g.sm + in % g.sm;
+    tn = block / g.bm * g.sn + in / g.sm;
+    return tm < g.tm && tn < g.tn;
+}
+
+template <bool kMX, bool kExact, int kRagged, int WT, int WN, int CT, int RT>
+__global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileGrid grid)
+{
+    constexpr int kWaves = WT * WN, BM = WT * CT * 32, BN = WN * RT * 32;
+    constexpr int kThreads = kWaves * 64, kStage = (BM + BN) * kStep;
+    static_assert(BM + BN == kThreads, "one thread stages one row's scales");
+    constexpr int kLoads = (BM + BN) / 8 / kWaves;  // of 8 rows, for each wave and step
+    static_assert(BM / 8 % kLoads == 0, "a wave loads rows of one operand");
+    constexpr int kScaled = BM + (kMX ? BN : WN);    // rows with scales in LDS (one for a wave's weight rows)
+    __shared__ __align__(1024) uint8_t lds[2 * kStage];
+    __shared__ __align__(16) uint32_t scales[3][4][kScaled];
+
+    int32_t tm, tn;
+    if (!tile_of(grid, tm, tn)) return;
+    int group = 0;
+    int32_t row0 = tm * BM, row_end = min(row0 + BM, a.m), k0 = 0, k1 = a.k;
+    if constexpr (kRagged == kRows) {
+        if (!find_row_tile(a, BM, tm, group, row0, row_end)) return;
+    } else if constexpr (kRagged == kContraction) {
+        group = blockIdx.y;
+        k0 = k_offset_at(a, group);
+        k1 = max(k0, k_offset_at(a, group + 1));
+    }
+    const int32_t col0 = tn * BN, col_end = min(col0 + BN, a.n);
+    const int32_t steps = (k1 - k0 + kStep - 1) / kStep;
+    const int32_t full = (k1 - k0) / kStep;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int wt = wave / WN, wn = wave % WN, p = lane & 31, h = lane >> 5;
+
+    // -- what this wave brings to LDS: kLoads times 8 rows of x or of w
+    const bool of_x = wave * kLoads * 8 < BM;
+    const int first = of_x ? wave * kLoads * 8 : wave * kLoads * 8 - BM;
+    const int64_t ld = of_x ? a.ldx : a.ldw;
+    const uint8_t *base = of_x ? a.x + (int64_t)row0 * a.ldx
+                               : a.w + (kRagged == kRows ? group * a.w_stride : 0) +
+                                     (int64_t)col0 * a.ldw;
+    const int last = (of_x ? row_end - row0 : col_end - col0) - 1;  // rows past it repeat it: their results are dropped
+    // Row r's 16-byte piece c lies at piece c ^ (r % 8) of its line in LDS: eight
+    // rows' pieces of one c, read together, then fall on all banks.
+    const uint32_t chunk = (lane & 7) ^ (lane >> 3);
+    uint32_t vrow = (lane >> 3) * (uint32_t)ld;
+    auto rows_at = [&](int i) { return (uint32_t)min(first + i * 8, last) * (uint32_t)ld; };
+    auto in_rows = [&](int i) {
+        return min(vrow, (uint32_t)max(min(last - first - i * 8, 7), 0) * (uint32_t)ld) + chunk * 16;
+    };
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t *>(base), 0, 0xFFFFFFFF, 0x00020000);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
+    auto fill = [&](int32_t s) {
+        const uint32_t to = (s & 1) * kStage + wave * kLoads * 1024;
+        const uint32_t from = (uint32_t)(k0 + s * kStep);
+        if (s < full) {
+            asm volatile("" : "+v"(vrow));  // eight addresses made anew take less than eight registers kept
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                load_to_lds(rsrc, lds0 + to + i * 1024, in_rows(i),
+                            __builtin_amdgcn_readfirstlane(rows_at(i) + from));
+        } else {  // what lies past the contraction's end counts as zero
+            const int have = k1 - k0 - s * kStep - (int32_t)chunk * 16;
+#pragma unroll 1  // once a tile, in few registers
+            for (int i = 0; i < kLoads; ++i) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                const uint8_t *q = base + (size_t)(rows_at(i) + in_rows(i)) + from;
+                if (have >= 16) v = *reinterpret_cast<const uint4 *>(q);
+                else if (kRagged == kContraction && have > 0) v = first_bytes(q, have);
+                *reinterpret_cast<uint4 *>(lds + to + i * 1024 + lane * 16) = v;
+            }
+        }
+    };
+
+    // -- scales: each thread one row, four steps at a time, two such groups of steps in
+    // turn.  The last group, which may be short, has a place of its own and is loaded
+    // ahead of the loop: inside there is no register for its many cases.
+    const int32_t last_group = (steps - 1) / 4;
+    const uint8_t *scale_row;
+    {
+        const bool x_row = tid < BM;
+        const int64_t gs = kRagged == kRows ? group * a.sw_stride : 0;
+        if constexpr (kMX) {
+            const int r = x_row ? row0 + min(tid, row_end - row0 - 1)
+                                : col0 + min(tid - BM, col_end - col0 - 1);
+            scale_row = (x_row ? static_cast<const uint8_t *>(a.sx) + (int64_t)r * a.ld_sx
+                               : static_cast<const uint8_t *>(a.sw) + gs + (int64_t)r * a.ld_sw) +
+                        k0 / 32;
+        } else {  // a wave's weight rows lie in one tile of 128 of their scales
+            const int r = x_row ? row0 + min(tid, row_end - row0 - 1)
+                                : min(col0 + min(tid - BM, WN - 1) * (RT * 32), a.n - 1) / 128;
+            scale_row = reinterpret_cast<const uint8_t *>(
+                x_row ? static_cast<const float *>(a.sx) + (int64_t)r * a.ld_sx
+                      : static_cast<const float *>(a.sw) + gs + (int64_t)r * a.ld_sw);
+        }
+    }
+    uint32_t sreg[4];
+    auto load_scales = [&](int32_t g) {  // a whole group
+        if (tid < kScaled) {
+            const Bytes16 v = *reinterpret_cast<const Bytes16 *>(scale_row + g * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sreg[i] = v.w[i];
+        }
+    };
+    auto store_scales = [&](int place) {
+        if (tid < kScaled) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) scales[place][i][tid] = sreg[i];
+        }
+    };
+    auto load_last_scales = [&]() {
+        if (tid < kScaled) {
+            const uint8_t *from = scale_row + last_group * 16;
+            const int have = kMX ? (k1 - k0 + 31) / 32 - last_group * 16 : steps * 4 - last_group * 16;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sreg[i] = 0;
+            for (int j = 0; j < 16; ++j)
+                if (j < have) {
+                    const uint32_t v = (uint32_t)from[j] << (j % 4 * 8);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (j / 4 == i) sreg[i] |= v;
+                }
+        }
+    };
+    // where step s finds them
+    auto scales_of = [&](int32_t s) { return scales[s / 4 == last_group ? 2 : s / 4 & 1][s & 3]; };
+
+    // -- operands: four places of a row's line, by the half of the step and of the operand
+    uint32_t at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) at[i] = p * kStep + (((2 * i + h) ^ (p & 7)) << 4);
+    auto operand = [&](uint32_t stage, int row, int t) {  // rows row .., half t
+        const uint8_t *q = lds + stage + row * kStep;
+        return join(*reinterpret_cast<const uint4 *>(q + at[2 * t]),
+                    *reinterpret_cast<const uint4 *>(q + at[2 * t + 1]));
+    };
+
+    f32x16 acc[RT][CT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[r][c][i] = 0.f;
+
+    // The products so far are in the accumulators here, not put off past a barrier with
+    // their operands still held.
+    auto settle = [&]() {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) asm volatile("" : "+v"(acc[r][c]));
+    };
+    // Step s is multiplied while step s + 1 comes into the other half of LDS.  A barrier
+    // in the middle of every step: behind it all of stage s is in registers, so its
+    // place takes step s + 2, and stage s + 1 is there to be read for the next step
+    // under this one's second half.  (What the last step reads ahead is not used.)
+    auto turn = [&](int32_t s) {
+        settle();
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        const bool scales_due = (s + 1) % 4 == 0 && (s + 1) / 4 < last_group;
+        if (scales_due) store_scales((s + 1) / 4 & 1);
+        __syncthreads();
+        if ((s + 1) % 4 == 0 && (s + 1) / 4 + 1 < last_group) load_scales((s + 1) / 4 + 1);
+        if (s + 2 < steps) fill(s + 2);
+    };
+    if (steps > 0) {
+        fill(0);
+        load_last_scales();
+        store_scales(2);
+        if (last_group > 0) {
+            load_scales(0);
+            store_scales(0);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (1 < last_group) load_scales(1);
+        if (1 < steps) fill(1);
+    }
+    if constexpr (kExact) {
+        for (int32_t s = 0; s < steps; ++s) {
+            const uint32_t stage = (s & 1) * kStage;
+            const uint32_t *sc = scales_of(s);
+            auto piece = [&](int row, int i) {  // 16 bytes of the wave's rows row ..
+                return *reinterpret_cast<const uint4 *>(lds + stage + row * kStep + at[i]);
+            };
+            if constexpr (kMX) {
+                uint32_t sx[CT], sr[RT];
+#pragma unroll
+                for (int c = 0; c < CT; ++c) sx[c] = sc[(wt * CT + c) * 32 + p];
+#pragma unroll
+                for (int r = 0; r < RT; ++r) sr[r] = sc[BM + (wn * RT + r) * 32 + p];
+                static_for<0, 4, 1>([&](auto I) {  // piece i of both halves: the step's group i
+                    constexpr int i = I;
+                    bf16x8 b[CT][2];
+#pragma unroll
+                    for (int c = 0; c < CT; ++c)
+                        decode16(b[c], piece((wt * CT + c) * 32, i), e8m0_to_f32((sx[c] >> (8 * i)) & 0xFF));
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        bf16x8 w[2];
+                        decode16(w, piece(BM + (wn * RT + r) * 32, i), e8m0_to_f32((sr[r] >> (8 * i)) & 0xFF));
+#pragma unroll
+                        for (int c = 0; c < CT; ++c)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                acc[r][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j], b[c][j], acc[r][c], 0, 0, 0);
+                    }
+                });
+            } else {
+                bf16x8 b[CT][4][2];
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) decode16(b[c][i], piece((wt * CT + c) * 32, i), 1.0f);
+                const float swv = __uint_as_float(sc[BM + wn]);
+                float f[CT];
+#pragma unroll
+                for (int c = 0; c < CT; ++c) f[c] = __uint_as_float(sc[(wt * CT + c) * 32 + p]) * swv;
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    bf16x8 w[4][2];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) decode16(w[i], piece(BM + (wn * RT + r) * 32, i), 1.0f);
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) {
+                        f32x16 q{};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                q = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[i][j], b[c][i][j], q, 0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            acc[r][c][i] = __builtin_fmaf(q[i], f[c], acc[r][c][i]);
+                    }
+                }
+            }
+            turn(s);
+        }
+    } else if constexpr (kMX) {
+        i32x8 b0[CT], b1[CT], w[RT];
+        auto fetch_b = [&](i32x8(&b)[CT], int32_t s, int t) {
+#pragma unroll
+            for (int c = 0; c < CT; ++c) b[c] = operand((s & 1) * kStage, (wt * CT + c) * 32, t);
+        };
+        auto fetch_w = [&](int r, int32_t s, int t) {
+            w[r] = operand((s & 1) * kStage, BM + (wn * RT + r) * 32, t);
+        };
+        if (steps > 0) {
+            fetch_b(b0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) fetch_w(r, 0, 0);
+        }
+        for (int32_t s = 0; s < steps; ++s) {
+            const uint32_t *sc = scales_of(s);
+            int sx[CT], sr[RT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) sx[c] = (int)(sc[(wt * CT + c) * 32 + p] >> (8 * h));
+#pragma unroll
+            for (int r = 0; r < RT; ++r) sr[r] = (int)(sc[BM + (wn * RT + r) * 32 + p] >> (8 * h));
+            fetch_b(b1, s, 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+                    acc[r][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        w[r], b0[c], acc[r][c], 0, 0, 0, sr[r], 0, sx[c]);
+                fetch_w(r, s, 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            turn(s);
+            fetch_b(b0, s + 1, 0);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+                    acc[r][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        w[r], b1[c], acc[r][c], 0, 0, 2, sr[r], 2, sx[c]);
+                fetch_w(r, s + 1, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    } else {
+        for (int32_t s = 0; s < steps; ++s) {
+            const uint32_t stage = (s & 1) * kStage;
+            const uint32_t *sc = scales_of(s);
+            const float swv = __uint_as_float(sc[BM + wn]);
+            float f[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) f[c] = __uint_as_float(sc[(wt * CT + c) * 32 + p]) * swv;
+            i32x8 b[CT][2];
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) b[c][t] = operand(stage, (wt * CT + c) * 32, t);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const i32x8 w0 = operand(stage, BM + (wn * RT + r) * 32, 0);
+                const i32x8 w1 = operand(stage, BM + (wn * RT + r) * 32, 1);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    f32x16 q{};
+                    q = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w0, b[c][0], q, 0, 0, 0, 0, 0, 0);
+                    q = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w1, b[c][1], q, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        acc[r][c][i] = __builtin_fmaf(q[i], f[c], acc[r][c][i]);
+                }
+            }
+            turn(s);
+        }
+    }
+
+    // -- out: a wave turns 32 tokens at a time around in LDS and writes their rows
+    __syncthreads();
+    // four neighbouring floats c / 4 of row r at place (c / 4) ^ (r % 8) of it: no bank
+    // is hit twice by eight rows
+    constexpr int kCols = RT * 32;
+    static_assert(kWaves * 32 * kCols * 4 <= 2 * kStage, "fits the stages");
+    float *out = reinterpret_cast<float *>(lds) + wave * 32 * kCols;
+    auto place = [&](int r, int c) { return out + r * kCols + (((c >> 2) ^ (r & 7)) << 2) + (c & 3); };
+    const int wcol = col0 + wn * kCols, cols = min(kCols, col_end - wcol);
+    const bool f32 = a.out_f32 != 0;
+    const int size = f32 ? 4 : 2;
+    uint8_t *y = static_cast<uint8_t *>(a.y) + (kRagged == kContraction ? group * a.y_stride * size : 0);
+    const bool wide = cols == kCols && (reinterpret_cast<uintptr_t>(y) & 15) == 0 && a.ldy * size % 16 == 0;
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<f32x4 *>(place(p, r * 32 + 8 * i + 4 * h)) =
+                    f32x4{acc[r][c][4 * i], acc[r][c][4 * i + 1], acc[r][c][4 * i + 2], acc[r][c][4 * i + 3]};
+        __builtin_amdgcn_wave_barrier();
+        const int32_t trow = row0 + (wt * CT + c) * 32;
+        const int rows = min(32, row_end - trow);
+        if (wide) {
+            constexpr int kPer = kCols / 4;  // lanes on a row
+#pragma unroll
+            for (int i = 0; i < 32 * kPer / 64; ++i) {
+                const int e = i * 64 + lane, tr = e / kPer, tc = e % kPer * 4;
+                if (tr < rows) {
+                    const f32x4 v = *reinterpret_cast<const f32x4 *>(place(tr, tc));
+                    const int64_t to = (int64_t)(trow + tr) * a.ldy + wcol + tc;
+                    if (f32)
+                        *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(y) + to) = v;
+                    else
+                        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(y) + to) =
+                            make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
+                }
+            }
+        } else if (cols > 0) {
+            for (int tr = 0; tr < rows; ++tr)
+                for (int tc = lane; tc < cols; tc += 64)
+                    store_product(y, (int64_t)(trow + tr) * a.ldy + wcol + tc, *place(tr, tc), f32);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+template <bool kMX, bool kExact, int kRagged, int WT, int WN, int CT, int RT>
+hipError_t launch(const Fp8Matmul &a, hipStream_t stream)
+{
+    constexpr int BM = WT * CT * 32, BN = WN * RT * 32;
+    TileGrid g;
+    g.tm = (a.m + BM - 1) / BM + (kRagged == kRows ? a.groups : 0);
+    g.tn = (a.n + BN - 1) / BN;
+    g.sm = g.tm < 8 ? g.tm : 8;
+    g.sn = 32 / g.sm < g.tn ? 32 / g.sm : g.tn;
+    g.bm = (g.tm + g.sm - 1) / g.sm;
+    const int64_t blocks = (int64_t)g.bm * ((g.tn + g.sn - 1) / g.sn);
+    const int64_t wgs = (blocks + 7) / 8 * 8 * g.sm * g.sn;
+    const int64_t groups = kRagged == kContraction ? a.groups : 1;
+    if (wgs > 0x7FFFFFFF || groups > 65535) return hipErrorInvalidConfiguration;
+    tile_kernel<kMX, kExact, kRagged, WT, WN, CT, RT>
+        <<<dim3((unsigned)wgs, (unsigned)groups), dim3(WT * WN * 64), 0, stream>>>(a, g);
+    return hipGetLastError();
+}
+
+template <bool kMX, int kRagged>
+hipError_t pick(const Fp8Matmul &a, hipStream_t stream)
+{
+    if (a.out_f32) return launch<kMX, true, kRagged, 2, 2, 2, 2>(a, stream);
+    const int64_t big = (int64_t)((a.m + 255) / 256) * ((a.n + 255) / 256) * (kRagged == kContraction ? a.groups : 1);
+    if (big >= 128 && kRagged != kContraction) return launch<kMX, false, kRagged, 4, 2, 2, 4>(a, stream);
+    return launch<kMX, false, kRagged, 2, 2, 2, 2>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_fp8_tiles(bool mx, int ragged, const Fp8Matmul &a, hipStream_t stream)
+{
+    if (mx)
+        return ragged == kDense ? pick<true, kDense>(a, stream)
+               : ragged == kRows ? pick<true, kRows>(a, stream)
+                                 : pick<true, kContraction>(a, stream);
+    return ragged == kDense ? pick<false, kDense>(a, stream) : pick<false, kRows>(a, stream);
+}
+
+}  // namespace mxq

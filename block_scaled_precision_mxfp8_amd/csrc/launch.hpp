@@ -99,6 +99,10 @@ hipError_t launch_fp4_matvec(bool nv, const uint16_t *x, int64_t tokens, int64_t
                              const uint8_t *q, const uint8_t *s, const float *g, int64_t n,
                              int64_t k, void *y, int64_t ldy, bool out_f32, hipStream_t stream);
 
+// Products with 8-bit operands (fp8_matmul.hpp); ragged: a Ragged.
+struct Fp8Matmul;
+hipError_t launch_fp8_tiles(bool mx, int ragged, const Fp8Matmul &a, hipStream_t stream);
+
 hipError_t launch_nvfp4_dequant(const uint8_t *q, const uint8_t *s, const float *g,
                                 int64_t rows, int64_t cols, uint16_t *out, hipStream_t stream);
 

@@ -10,6 +10,7 @@
 
 #include <vector>
 
+#include "fp8_matmul.hpp"
 #include "kv4.hpp"
 #include "launch.hpp"
 #include "mxq.h"
@@ -252,6 +253,57 @@ bool kv_shape_ok(int32_t heads, int32_t dim, int32_t page)
 }
 
 // Checks a cache description (its data pointer only when it has pages).
+// What the five products with 8-bit operands share; `ragged` is what offsets cut.
+mxq_status fp8_matmul(bool mx, int ragged, const mxq_matmul_args *p, void *stream)
+{
+    if (!p || p->reserved != 0) return MXQ_EINVAL;
+    if (p->m < 0 || p->n < 0 || p->k < 0 || p->groups < 0 || p->ldx < 0 || p->ldw < 0 ||
+        p->ld_sx < 0 || p->ld_sw < 0 || p->ldy < 0 || p->w_group_stride < 0 ||
+        p->sw_group_stride < 0 || p->y_group_stride < 0)
+        return MXQ_EINVAL;
+    if (ragged == mxq::kDense && (p->groups != 0 || p->offsets)) return MXQ_EINVAL;
+    if (p->k % (mx ? 32 : 16) != 0 && ragged != mxq::kContraction) return MXQ_ESHAPE;
+    if (p->m == 0 || p->n == 0 || (ragged != mxq::kDense && p->groups == 0)) return MXQ_OK;
+    if (!p->y || (ragged != mxq::kDense && !p->offsets)) return MXQ_EINVAL;
+    if (p->k > 0 && (!p->x || !p->w || !p->sx || !p->sw)) return MXQ_EINVAL;
+    const int64_t blocks = (p->k + (mx ? 31 : 127)) / (mx ? 32 : 128);
+    if (p->ldx < p->k || p->ldw < p->k || p->ld_sx < blocks || p->ld_sw < blocks || p->ldy < p->n)
+        return MXQ_ESHAPE;
+    if (!aligned(p->x, 16) || !aligned(p->w, 16) || p->ldx % 16 || p->ldw % 16 ||
+        p->w_group_stride % 16 || !aligned(p->sx, mx ? 1 : 4) || !aligned(p->sw, mx ? 1 : 4) ||
+        !aligned(p->y, p->out_fp32 ? 4 : 2) || !aligned(p->offsets, 4))
+        return MXQ_EALIGN;
+    // rows of a tile are reached with 32-bit offsets, everything else with 64
+    constexpr int64_t most = 0x7FFFFF00, most_ld = (int64_t)1 << 22;
+    if (p->m > most || p->n > most || p->ldx > most_ld || p->ldw > most_ld ||
+        p->groups > 65535 || !fits(p->m, p->ld_sx) || !fits(p->n, p->ld_sw) ||
+        !fits(p->m, p->ldy) || !fits(p->groups, p->w_group_stride) ||
+        !fits(p->groups, p->sw_group_stride) || !fits(p->groups, p->y_group_stride))
+        return MXQ_ESIZE;
+    mxq::Fp8Matmul a{};
+    a.x = p->x;
+    a.w = p->w;
+    a.sx = p->sx;
+    a.sw = p->sw;
+    a.y = p->y;
+    a.offsets = p->offsets;
+    a.ldx = p->ldx;
+    a.ldw = p->ldw;
+    a.ld_sx = p->ld_sx;
+    a.ld_sw = p->ld_sw;
+    a.ldy = p->ldy;
+    a.w_stride = p->w_group_stride;
+    a.sw_stride = p->sw_group_stride;
+    a.y_stride = p->y_group_stride;
+    a.m = (int32_t)p->m;
+    a.n = (int32_t)p->n;
+    a.k = (int32_t)p->k;
+    a.groups = p->groups;
+    a.out_f32 = p->out_fp32 != 0;
+    const hipError_t e = mxq::launch_fp8_tiles(mx, ragged, a, as_stream(stream));
+    return e == hipErrorInvalidConfiguration ? MXQ_ESIZE : from_hip(e);
+}
+
 mxq_status check_kv(const mxq_kv_cache *c, mxq::Kv4Geom &geo)
 {
     if (!c || c->pages < 0 || c->reserved != 0) return MXQ_EINVAL;
@@ -700,6 +752,31 @@ mxq_status nvfp4_matvec(const uint16_t *x, int64_t tokens, int64_t ldx, const ui
                         int64_t ldy, int out_fp32, void *stream)
 {
     return fp4_matvec(true, x, tokens, ldx, q, s, g, n, k, y, ldy, out_fp32, stream);
+}
+
+mxq_status blockfp8_matmul(const mxq_matmul_args *args, void *stream)
+{
+    return fp8_matmul(false, mxq::kDense, args, stream);
+}
+
+mxq_status mxq_matmul(const mxq_matmul_args *args, void *stream)
+{
+    return fp8_matmul(true, mxq::kDense, args, stream);
+}
+
+mxq_status blockfp8_matmul_grouped(const mxq_matmul_args *args, void *stream)
+{
+    return fp8_matmul(false, mxq::kRows, args, stream);
+}
+
+mxq_status mxq_matmul_grouped(const mxq_matmul_args *args, void *stream)
+{
+    return fp8_matmul(true, mxq::kRows, args, stream);
+}
+
+mxq_status mxq_matmul_wgrad(const mxq_matmul_args *args, void *stream)
+{
+    return fp8_matmul(true, mxq::kContraction, args, stream);
 }
 
 size_t mxfp4_kv_page_bytes(int32_t kv_heads, int32_t head_dim, int32_t page_size)

@@ -489,6 +489,65 @@ mxq_status nvfp4_matvec(const uint16_t *x, int64_t tokens, int64_t ldx, const ui
                         int64_t ldy, int out_fp32, void *stream);
 
 /*
+ * Products of 8-bit tokens with 8-bit weights (blockfp8_*: block-FP8, mxq_*:
+ * MXFP8), summed in fp32, rounded once:
+ *   y[i, j] = sum_k x[i, k] w[j, k]
+ * x [m, k] and w [n, k] are E4M3 codes, row strides ldx and ldw bytes, 16-byte
+ * aligned, strides multiples of 16 and at most 2^22.  Scales, row strides
+ * ld_sx and ld_sw elements:
+ *   block-FP8  sx fp32 [m, ceil(k/128)], one for 128 values of a row (as
+ *              blockfp8_quantize_1x128 writes them); sw fp32 [ceil(n/128),
+ *              ceil(k/128)], one for 128 x 128 (as blockfp8_quantize); 4-byte aligned
+ *   MXFP8      sx E8M0 [m, k/32], sw E8M0 [n, k/32] (as mxq_quantize_rowwise or,
+ *              of transposed matrices, mxq_quantize_colwise_t); any alignment
+ * y [m, n] is bf16, or fp32 when out_fp32 != 0, row stride ldy elements, aligned
+ * to its element (rows of 16-byte multiples are written faster).  k % 16 == 0
+ * (block-FP8) or k % 32 == 0 (MXFP8), MXQ_ESHAPE otherwise; any m, n >= 0; k == 0
+ * writes zeros.  The gradient of x is the product of y's gradient, quantized
+ * along n, with the transposed weights: 128 x 128 tiles and their scales may be
+ * transposed as they are.
+ *
+ * Grouped forms: offsets is int32 [groups + 1] on the device and does not
+ * decrease (values outside the rows are taken as the nearest end; what other
+ * offsets give is unspecified, but stays inside y).
+ *   *_matmul_grouped  rows offsets[g] .. offsets[g + 1] - 1 of x are multiplied
+ *       with the g-th weights, w + g * w_group_stride bytes (a multiple of 16)
+ *       with sw + g * sw_group_stride elements.  Rows before the first and
+ *       behind the last offset are left as they were.
+ *   mxq_matmul_wgrad  k is cut: y + g * y_group_stride elements = the sum over k
+ *       in offsets[g] .. offsets[g + 1] - 1, zeros for an empty group.  Offsets are
+ *       multiples of 32 or k itself (others count as the multiple below); k may
+ *       then be anything, and scales are [m, ceil(k/32)], [n, ceil(k/32)].  With x = the
+ *       transposed gradient [out, tokens] and w = the transposed input [in,
+ *       tokens], both from mxq_quantize_colwise_t, y is a linear layer's weight
+ *       gradient [groups, out, in].
+ * At most 65535 groups; offsets and groups are NULL and 0 for the dense forms.
+ * NaN codes and scales reach the sums they belong to.  The order of summation
+ * depends on shapes alone; sums of MXFP8 are kept in the matrix cores, whose
+ * fp32 additions cut off what they cannot hold (block-FP8: within 128 k).
+ */
+typedef struct mxq_matmul_args {
+    const uint8_t *x;
+    const void *sx;
+    int64_t ldx, ld_sx;
+    const uint8_t *w;
+    const void *sw;
+    int64_t ldw, ld_sw, w_group_stride, sw_group_stride;
+    void *y;
+    int64_t ldy, y_group_stride;
+    const int32_t *offsets;
+    int64_t m, n, k;
+    int32_t groups, out_fp32;
+    int64_t reserved; /* set to 0 */
+} mxq_matmul_args;
+
+mxq_status blockfp8_matmul(const mxq_matmul_args *args, void *stream);
+mxq_status mxq_matmul(const mxq_matmul_args *args, void *stream);
+mxq_status blockfp8_matmul_grouped(const mxq_matmul_args *args, void *stream);
+mxq_status mxq_matmul_grouped(const mxq_matmul_args *args, void *stream);
+mxq_status mxq_matmul_wgrad(const mxq_matmul_args *args, void *stream);
+
+/*
  * A key/value cache held in MXFP4, in pages.  One layer of it is a device
  * buffer of `pages` pages, page_stride bytes apart (16-byte aligned, a
  * multiple of 16, at least mxfp4_kv_page_bytes).  A page is a run of bytes
