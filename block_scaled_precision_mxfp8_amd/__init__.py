@@ -90,6 +90,10 @@ SIGNATURES = {
     "nvfp4_quantize_grouped_plan": (ctypes.c_int, [_vp, _vp, _vp, _sz, _vp]),
     "mxfp4_matvec": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, ctypes.c_int, _vp]),
     "nvfp4_matvec": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i64, ctypes.c_int, _vp]),
+    "blockfp8_rmsnorm": (ctypes.c_int, [_vp, _vp]),
+    "mxq_rmsnorm": (ctypes.c_int, [_vp, _vp]),
+    "mxq_rmsnorm_backward_workspace_size": (_sz, [_i64, _i64]),
+    "mxq_rmsnorm_backward": (ctypes.c_int, [_vp, _vp]),
     "blockfp8_matmul": (ctypes.c_int, [_vp, _vp]),
     "mxq_matmul": (ctypes.c_int, [_vp, _vp]),
     "blockfp8_matmul_grouped": (ctypes.c_int, [_vp, _vp]),
@@ -725,4 +729,5 @@ from .decode import (KVPagePool, mxfp4_kv_append, mxfp4_kv_attention, mxfp4_kv_c
 # ---------------------------------------------------------------------------
 
 from .linear import (blockfp8_matmul, blockfp8_matmul_grouped, mxfp8_matmul,  # noqa: E402
-                     mxfp8_matmul_grouped, mxfp8_matmul_wgrad)
+                     mxfp8_matmul_grouped, mxfp8_matmul_wgrad, rmsnorm_backward, rmsnorm_blockfp8,
+                     rmsnorm_mxfp8)

@@ -91,9 +91,66 @@ __device__ __forceinline__ bool find_row_tile(const Fp8Matmul &a, int rows, int3
     return false;
 }
 
+constexpr int kStep = 128;  // k of one step: one line of every row
+
+// 64 lanes' 16 bytes at base + voff + soff into LDS at `lds` + 16 * lane, with no
+// register in between.  In assembly because the compiler would have every later read
+// of LDS wait for it; the loops wait where they have to.  (m0 is set right before
+// its use, and the compiler has none of its own for it here.)
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds,
+                                            uint32_t voff, uint32_t soff)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "memory");
+}
+
+__device__ __forceinline__ i32x8 join(uint4 a, uint4 b)
+{
+    return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+// 16 codes times a power of two (1 or an MXFP8 scale) as bf16: exact wherever bf16 holds the value.
+__device__ __forceinline__ void decode16(bf16x8 (&d)[2], uint4 q, float scale)
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint2 a = mx_dequant4_hw(w[2 * j], scale), b = mx_dequant4_hw(w[2 * j + 1], scale);
+        d[j] = __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, b.x, b.y));
+    }
+}
+
 // 16 bytes at any address
 struct __attribute__((packed, aligned(1))) Bytes16 { uint32_t w[4]; };
-struct __attribute__((packed, aligned(4))) Words4 { uint32_t w[4]; };
+
+// Bytes at .. at + 15 of a run of `total`, zeros behind its end; reads nothing
+// outside the run.  Near the end the run's last 16 bytes are read and moved down: one
+// load, where a load for each byte would take the load path many times as long.
+__device__ __forceinline__ uint4 bytes16_of(const uint8_t *run, int32_t at, int32_t total)
+{
+    if (total < 16) return first_bytes(run + at, max(min(total - at, 15), 0));
+    const int over = max(at + 16 - total, 0);
+    const Bytes16 v = *reinterpret_cast<const Bytes16 *>(run + (at - over));
+    uint64_t lo = v.w[0] | (uint64_t)v.w[1] << 32, hi = v.w[2] | (uint64_t)v.w[3] << 32;
+    if (over >= 8) lo = hi, hi = 0;
+    const int bits = 8 * (over & 7);
+    if (bits) {
+        lo = lo >> bits | hi << (64 - bits);
+        hi >>= bits;
+    }
+    if (over >= 16) lo = 0;
+    return make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
+}
+
+// A buffer of 2^31 - 1 bytes from p on: an offset of kNowhere is outside it, and what
+// is loaded from there is zero.
+constexpr uint32_t kNowhere = 0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const uint8_t *p)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, 0x7FFFFFFF, 0x00020000);
+}
 
 __device__ __forceinline__ void store_product(void *y, int64_t at, float v, bool f32)
 {

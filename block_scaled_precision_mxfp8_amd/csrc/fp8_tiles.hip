@@ -23,37 +23,6 @@ namespace mxq {
 
 namespace {
 
-constexpr int kStep = 128;  // k of one step: one line of every row
-
-// 64 lanes' 16 bytes at base + voff + soff into LDS at `lds` + 16 * lane, with no
-// register in between.  In assembly because the compiler would have every later read
-// of LDS wait for it; the loop below waits where it has to.  (m0 is set right before
-// its use, and the compiler has none of its own for it here.)
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds,
-                                            uint32_t voff, uint32_t soff)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :
-                 : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-                 : "memory");
-}
-
-__device__ __forceinline__ i32x8 join(uint4 a, uint4 b)
-{
-    return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
-}
-
-// 16 codes times a power of two (1 or an MXFP8 scale) as bf16: exact wherever bf16 holds the value.
-__device__ __forceinline__ void decode16(bf16x8 (&d)[2], uint4 q, float scale)
-{
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint2 a = mx_dequant4_hw(w[2 * j], scale), b = mx_dequant4_hw(w[2 * j + 1], scale);
-        d[j] = __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, b.x, b.y));
-    }
-}
-
 struct TileGrid {
     int32_t tm, tn;  // tiles of rows (at most, if grouped) and of columns
     int32_t sm, sn;  // tiles of a block that one XCD works on at a time
@@ -116,28 +85,29 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
     uint32_t vrow = (lane >> 3) * (uint32_t)ld;
     auto rows_at = [&](int i) { return (uint32_t)min(first + i * 8, last) * (uint32_t)ld; };
     auto in_rows = [&](int i) {
-        return min(vrow, (uint32_t)max(min(last - first - i * 8, 7), 0) * (uint32_t)ld) + chunk * 16;
+        return min(vrow, (uint32_t)__builtin_amdgcn_readfirstlane(max(min(last - first - i * 8, 7), 0) * (int)ld)) +
+               chunk * 16;
     };
-    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t *>(base), 0, 0xFFFFFFFF, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rsrc = buffer_at(base);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
     auto fill = [&](int32_t s) {
         const uint32_t to = (s & 1) * kStage + wave * kLoads * 1024;
         const uint32_t from = (uint32_t)(k0 + s * kStep);
-        if (s < full) {
+        const int have = k1 - k0 - s * kStep - (int32_t)chunk * 16;
+        if (kRagged != kContraction || s < full || (k1 & 15) == 0) {
             asm volatile("" : "+v"(vrow));  // eight addresses made anew take less than eight registers kept
+            const uint32_t past = have < 16 ? kNowhere : 0u;  // what lies past the contraction's end is zero
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
-                load_to_lds(rsrc, lds0 + to + i * 1024, in_rows(i),
+                load_to_lds(rsrc, lds0 + to + i * 1024, in_rows(i) | past,
                             __builtin_amdgcn_readfirstlane(rows_at(i) + from));
-        } else {  // what lies past the contraction's end counts as zero
-            const int have = k1 - k0 - s * kStep - (int32_t)chunk * 16;
-#pragma unroll 1  // once a tile, in few registers
+        } else {  // it ends inside 16 bytes
+#pragma unroll 1
             for (int i = 0; i < kLoads; ++i) {
                 uint4 v = make_uint4(0, 0, 0, 0);
                 const uint8_t *q = base + (size_t)(rows_at(i) + in_rows(i)) + from;
                 if (have >= 16) v = *reinterpret_cast<const uint4 *>(q);
-                else if (kRagged == kContraction && have > 0) v = first_bytes(q, have);
+                else if (have > 0) v = first_bytes(q, have);
                 *reinterpret_cast<uint4 *>(lds + to + i * 1024 + lane * 16) = v;
             }
         }
@@ -179,19 +149,11 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
             for (int i = 0; i < 4; ++i) scales[place][i][tid] = sreg[i];
         }
     };
-    auto load_last_scales = [&]() {
+    auto load_last_scales = [&]() {  // zeros behind the row's end
         if (tid < kScaled) {
-            const uint8_t *from = scale_row + last_group * 16;
-            const int have = kMX ? (k1 - k0 + 31) / 32 - last_group * 16 : steps * 4 - last_group * 16;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sreg[i] = 0;
-            for (int j = 0; j < 16; ++j)
-                if (j < have) {
-                    const uint32_t v = (uint32_t)from[j] << (j % 4 * 8);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (j / 4 == i) sreg[i] |= v;
-                }
+            const int32_t have = kMX ? (k1 - k0 + 31) / 32 : steps * 4, before = kMX ? k0 / 32 : 0;
+            const uint4 v = bytes16_of(scale_row - before, before + last_group * 16, before + have);
+            sreg[0] = v.x, sreg[1] = v.y, sreg[2] = v.z, sreg[3] = v.w;
         }
     };
     // where step s finds them
@@ -464,8 +426,12 @@ hipError_t pick(const Fp8Matmul &a, hipStream_t stream)
 
 }  // namespace
 
-hipError_t launch_fp8_tiles(bool mx, int ragged, const Fp8Matmul &a, hipStream_t stream)
+hipError_t launch_fp8_matmul(bool mx, int ragged, const Fp8Matmul &a, hipStream_t stream)
 {
+    if (ragged != kContraction) {
+        const int tokens = ragged == kRows ? 2 * ((a.m - 1) / a.groups + 1) : a.m;
+        if (tokens <= 64) return launch_fp8_few(mx, ragged, tokens, a, stream);
+    }
     if (mx)
         return ragged == kDense ? pick<true, kDense>(a, stream)
                : ragged == kRows ? pick<true, kRows>(a, stream)

@@ -101,7 +101,36 @@ hipError_t launch_fp4_matvec(bool nv, const uint16_t *x, int64_t tokens, int64_t
 
 // Products with 8-bit operands (fp8_matmul.hpp); ragged: a Ragged.
 struct Fp8Matmul;
-hipError_t launch_fp8_tiles(bool mx, int ragged, const Fp8Matmul &a, hipStream_t stream);
+hipError_t launch_fp8_matmul(bool mx, int ragged, const Fp8Matmul &a, hipStream_t stream);
+// for up to 64 tokens, or about as many in a group
+hipError_t launch_fp8_few(bool mx, int ragged, int tokens, const Fp8Matmul &a, hipStream_t stream);
+
+// RMS norm with 8-bit output, and its gradient; every output but q, scale, dx and
+// dweight may be null, and so may residual and dh.  h, y, q, dx are contiguous.
+constexpr int64_t kRmsNormMostCols = 16384;
+struct RmsNorm {
+    const uint16_t *x, *residual;
+    const void *weight;
+    uint8_t *q;
+    void *scale;
+    uint16_t *h, *y;
+    float *rstd;
+    int64_t rows, cols, ldx, ldr;
+    float eps;
+    int32_t weight_f32;
+};
+struct RmsNormBack {
+    const uint16_t *dy, *h, *dh;
+    const void *weight;
+    const float *rstd;
+    uint16_t *dx;
+    float *dweight, *part;  // part: rmsnorm_back_parts rows of cols
+    int64_t rows, cols, ld_dy, ldh, ld_dh;
+    int32_t weight_f32;
+};
+hipError_t launch_rmsnorm(bool mx, const RmsNorm &a, hipStream_t stream);
+int32_t rmsnorm_back_parts(int64_t rows, int64_t cols);
+hipError_t launch_rmsnorm_back(const RmsNormBack &a, hipStream_t stream);
 
 hipError_t launch_nvfp4_dequant(const uint8_t *q, const uint8_t *s, const float *g,
                                 int64_t rows, int64_t cols, uint16_t *out, hipStream_t stream);

@@ -253,6 +253,41 @@ bool kv_shape_ok(int32_t heads, int32_t dim, int32_t page)
 }
 
 // Checks a cache description (its data pointer only when it has pages).
+mxq_status rmsnorm(bool mx, const mxq_rmsnorm_args *p, void *stream)
+{
+    if (!p || p->reserved != 0) return MXQ_EINVAL;
+    if (p->rows < 0 || p->cols < 0 || p->ldx < 0 || p->ld_residual < 0) return MXQ_EINVAL;
+    if (p->cols % (mx ? 32 : 8) != 0) return MXQ_ESHAPE;
+    if (p->rows == 0 || p->cols == 0) return MXQ_OK;
+    if (!p->x || !p->weight || !p->q || !p->scale || (p->residual && !p->h)) return MXQ_EINVAL;
+    if (p->ldx < p->cols || (p->residual && p->ld_residual < p->cols)) return MXQ_ESHAPE;
+    if (!aligned(p->x, 16) || p->ldx % 8 || !aligned(p->residual, 16) ||
+        (p->residual && p->ld_residual % 8) || !aligned(p->weight, 16) || !aligned(p->q, 8) ||
+        !aligned(p->scale, mx ? 1 : 4) || !aligned(p->h, 16) || !aligned(p->y, 16) ||
+        !aligned(p->rstd, 4))
+        return MXQ_EALIGN;
+    if (p->cols > mxq::kRmsNormMostCols || !fits(p->rows, p->ldx) ||
+        (p->residual && !fits(p->rows, p->ld_residual)) || !fits(p->rows, 2 * p->cols))
+        return MXQ_ESIZE;
+    mxq::RmsNorm a{};
+    a.x = p->x;
+    a.residual = p->residual;
+    a.weight = p->weight;
+    a.q = p->q;
+    a.scale = p->scale;
+    a.h = p->h;
+    a.y = p->y;
+    a.rstd = p->rstd;
+    a.rows = p->rows;
+    a.cols = p->cols;
+    a.ldx = p->ldx;
+    a.ldr = p->ld_residual;
+    a.eps = p->eps;
+    a.weight_f32 = p->weight_fp32 != 0;
+    const hipError_t e = mxq::launch_rmsnorm(mx, a, as_stream(stream));
+    return e == hipErrorInvalidConfiguration ? MXQ_ESIZE : from_hip(e);
+}
+
 // What the five products with 8-bit operands share; `ragged` is what offsets cut.
 mxq_status fp8_matmul(bool mx, int ragged, const mxq_matmul_args *p, void *stream)
 {
@@ -300,7 +335,7 @@ mxq_status fp8_matmul(bool mx, int ragged, const mxq_matmul_args *p, void *strea
     a.k = (int32_t)p->k;
     a.groups = p->groups;
     a.out_f32 = p->out_fp32 != 0;
-    const hipError_t e = mxq::launch_fp8_tiles(mx, ragged, a, as_stream(stream));
+    const hipError_t e = mxq::launch_fp8_matmul(mx, ragged, a, as_stream(stream));
     return e == hipErrorInvalidConfiguration ? MXQ_ESIZE : from_hip(e);
 }
 
@@ -752,6 +787,61 @@ mxq_status nvfp4_matvec(const uint16_t *x, int64_t tokens, int64_t ldx, const ui
                         int64_t ldy, int out_fp32, void *stream)
 {
     return fp4_matvec(true, x, tokens, ldx, q, s, g, n, k, y, ldy, out_fp32, stream);
+}
+
+mxq_status blockfp8_rmsnorm(const mxq_rmsnorm_args *args, void *stream)
+{
+    return rmsnorm(false, args, stream);
+}
+
+mxq_status mxq_rmsnorm(const mxq_rmsnorm_args *args, void *stream)
+{
+    return rmsnorm(true, args, stream);
+}
+
+size_t mxq_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols)
+{
+    if (rows <= 0 || cols <= 0 || cols > mxq::kRmsNormMostCols) return 0;
+    return (size_t)mxq::rmsnorm_back_parts(rows, cols) * cols * sizeof(float);
+}
+
+mxq_status mxq_rmsnorm_backward(const mxq_rmsnorm_backward_args *p, void *stream)
+{
+    if (!p || p->reserved != 0) return MXQ_EINVAL;
+    if (p->rows < 0 || p->cols < 0 || p->ld_dy < 0 || p->ldh < 0 || p->ld_dh < 0) return MXQ_EINVAL;
+    if (p->cols % 8 != 0) return MXQ_ESHAPE;
+    if (p->cols == 0) return MXQ_OK;
+    if (!p->dweight || (p->rows > 0 && (!p->dy || !p->h || !p->weight || !p->rstd || !p->dx)))
+        return MXQ_EINVAL;
+    if (p->rows > 0 && (p->ld_dy < p->cols || p->ldh < p->cols || (p->dh && p->ld_dh < p->cols)))
+        return MXQ_ESHAPE;
+    if (!aligned(p->dy, 16) || p->ld_dy % 8 || !aligned(p->h, 16) || p->ldh % 8 ||
+        !aligned(p->dh, 16) || (p->dh && p->ld_dh % 8) || !aligned(p->weight, 16) ||
+        !aligned(p->rstd, 4) || !aligned(p->dx, 16) || !aligned(p->dweight, 4) ||
+        !aligned(p->workspace, 16))
+        return MXQ_EALIGN;
+    if (p->cols > mxq::kRmsNormMostCols || !fits(p->rows, p->ld_dy) || !fits(p->rows, p->ldh) ||
+        (p->dh && !fits(p->rows, p->ld_dh)) || !fits(p->rows, 2 * p->cols))
+        return MXQ_ESIZE;
+    const size_t need = mxq_rmsnorm_backward_workspace_size(p->rows, p->cols);
+    if (need > 0 && !p->workspace) return MXQ_EINVAL;
+    if (p->workspace_bytes < need) return MXQ_ESIZE;
+    mxq::RmsNormBack a{};
+    a.dy = p->dy;
+    a.h = p->h;
+    a.dh = p->dh;
+    a.weight = p->weight;
+    a.rstd = p->rstd;
+    a.dx = p->dx;
+    a.dweight = p->dweight;
+    a.part = static_cast<float *>(p->workspace);
+    a.rows = p->rows;
+    a.cols = p->cols;
+    a.ld_dy = p->ld_dy;
+    a.ldh = p->ldh;
+    a.ld_dh = p->ld_dh;
+    a.weight_f32 = p->weight_fp32 != 0;
+    return from_hip(mxq::launch_rmsnorm_back(a, as_stream(stream)));
 }
 
 mxq_status blockfp8_matmul(const mxq_matmul_args *args, void *stream)

@@ -16,13 +16,23 @@ import torch
 import block_scaled_precision_mxfp8_amd as _mxq
 from .decode import _as_bytes, _need, _stream_of
 
-# mxq_matmul_args as bytes
+# mxq_matmul_args, mxq_rmsnorm_args and mxq_rmsnorm_backward_args as bytes: packing
+# them costs a fraction of filling a ctypes structure field by field
 _MATMUL = struct.Struct("@PPqqPPqqqqPqqPqqqiiq")
+_RMSNORM = struct.Struct("@PPPPPPPPqqqqfiq")
+_RMSNORM_BACKWARD = struct.Struct("@PPPPPPPPNqqqqqii")
 
 
-def _on(device: torch.device):
-    """Makes ``device`` current for a launch where it is not."""
-    return torch.cuda.device(device)
+def _call(fn: str, device: torch.device, args: bytes):
+    """One library call on the current stream of ``device``, made current where it is not."""
+    f = getattr(_mxq._lib or _mxq.load(), fn)
+    if device.index == torch.cuda.current_device():
+        st = f(args, _stream_of(device))
+    else:
+        with torch.cuda.device(device):
+            st = f(args, _stream_of(device))
+    if st:
+        raise _mxq.MXQError(fn, st)
 
 
 def _codes(t, what: str, dims: int, device=None) -> torch.Tensor:
@@ -79,20 +89,11 @@ def _offsets(offsets, device) -> torch.Tensor:
 
 
 def _launch(fn: str, x, sx, w, sw, y, n: int, k: int, offsets=None, w_stride=0, sw_stride=0, y_stride=0):
-    L = _mxq._lib or _mxq.load()
-    args = _MATMUL.pack(
+    _call(fn, x.device, _MATMUL.pack(
         x.data_ptr(), sx.data_ptr(), x.stride(0), sx.stride(0), w.data_ptr(), sw.data_ptr(),
         w.stride(-2), sw.stride(-2), w_stride, sw_stride, y.data_ptr(), n, y_stride,
         0 if offsets is None else offsets.data_ptr(), x.shape[0], n, k,
-        0 if offsets is None else offsets.shape[0] - 1, y.dtype is torch.float32, 0)
-    dev = x.device
-    if dev.index == torch.cuda.current_device():
-        st = getattr(L, fn)(args, _stream_of(dev))
-    else:
-        with _on(dev):
-            st = getattr(L, fn)(args, _stream_of(dev))
-    if st:
-        raise _mxq.MXQError(fn, st)
+        0 if offsets is None else offsets.shape[0] - 1, y.dtype is torch.float32, 0))
     return y
 
 
@@ -185,3 +186,111 @@ def mxfp8_matmul_wgrad(dyt: torch.Tensor, dys: torch.Tensor, xt: torch.Tensor, x
     offsets = _offsets(offsets, dev)
     y = _out(out, (offsets.shape[0] - 1, n, k), out_dtype, dev)
     return _launch("mxq_matmul_wgrad", dyt, dys, xt, xs, y, k, tokens, offsets, y_stride=n * k)
+
+
+# ---------------------------------------------------------------------------
+# RMS norm
+# ---------------------------------------------------------------------------
+
+def _rows(t, what: str, shape, device=None) -> torch.Tensor:
+    """bf16 [..., cols] as 2-D with 16-byte aligned rows (a copy if it has none)."""
+    if device is None:
+        _mxq._need_bf16_cuda(t, what)
+    else:
+        _need(t, what, torch.bfloat16, device)
+    if t.dim() < 1:
+        raise ValueError(f"{what} must be [..., cols]")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {list(shape)}, not {list(t.shape)}")
+    if t.dim() != 2:
+        t = t.reshape(t.shape[:-1].numel(), t.shape[-1])
+    ld, unit = t.stride()
+    if unit != 1 or ld % 8 or ld < t.shape[1] or t.data_ptr() % 16:
+        t = t.clone(memory_format=torch.contiguous_format)
+    return t
+
+
+def _norm_weight(weight, cols: int, device) -> torch.Tensor:
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("weight must be a bfloat16 or float32 tensor")
+    if weight.device != device:
+        raise ValueError(f"weight must be on {device}")
+    if tuple(weight.shape) != (cols,):
+        raise ValueError(f"weight must be [{cols}]")
+    if not weight.is_contiguous() or weight.data_ptr() % 16:
+        weight = weight.clone(memory_format=torch.contiguous_format)
+    return weight
+
+
+def _rmsnorm(fn: str, mx: bool, x, weight, residual, eps, return_rstd, return_normed):
+    shape = x.shape if isinstance(x, torch.Tensor) else None
+    x2 = _rows(x, "x", None)
+    dev = x2.device
+    rows, cols = x2.shape
+    step = 32 if mx else 8
+    if cols % step:
+        raise ValueError(f"x must have a multiple of {step} columns, not {cols}")
+    weight = _norm_weight(weight, cols, dev)
+    r2 = h = rstd = y = None
+    if residual is not None:
+        r2 = _rows(residual, "residual", shape, dev)
+        h = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+    scale = torch.empty((rows, cols // 32 if mx else -(-cols // 128)),
+                        dtype=torch.uint8 if mx else torch.float32, device=dev)
+    if return_rstd:
+        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+    if return_normed:
+        y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _call(fn, dev, _RMSNORM.pack(
+        x2.data_ptr(), 0 if r2 is None else r2.data_ptr(), weight.data_ptr(), q.data_ptr(), scale.data_ptr(),
+        0 if h is None else h.data_ptr(), 0 if y is None else y.data_ptr(), 0 if rstd is None else rstd.data_ptr(),
+        rows, cols, x2.stride(0), 0 if r2 is None else r2.stride(0), eps, weight.dtype is torch.float32, 0))
+    return tuple(t for t in (q, scale, h, rstd, y) if t is not None)
+
+
+def rmsnorm_blockfp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                     eps: float = 1e-6, return_rstd: bool = False, return_normed: bool = False):
+    """RMS norm of x [..., cols] bf16 (any row stride), the residual of its shape
+    added first, with 1 x 128 block-FP8 output: (q uint8 [rows, cols], S float32
+    [rows, ceil(cols/128)]), then, as asked for, h = bf16(x + residual) (with a
+    residual), 1 / rms float32 [rows], and the normed values in bf16.  weight [cols] is
+    bf16 or fp32; cols a multiple of 8, at most 16384."""
+    return _rmsnorm("blockfp8_rmsnorm", False, x, weight, residual, eps, return_rstd, return_normed)
+
+
+def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                  eps: float = 1e-6, return_rstd: bool = False, return_normed: bool = False):
+    """rmsnorm_blockfp8 with row-wise MXFP8 output (q uint8 [rows, cols], scale uint8
+    [rows, cols/32]); cols a multiple of 32."""
+    return _rmsnorm("mxq_rmsnorm", True, x, weight, residual, eps, return_rstd, return_normed)
+
+
+def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                     dh: torch.Tensor | None = None):
+    """The norm's gradient, the quantizer counted as the identity: dy, h (x, or h as
+    the norm returned it) and dh (the gradient that reaches h past the norm) bf16 [...,
+    cols], rstd float32 [rows] as returned: (dx bf16 of dy's shape, the gradient of x
+    and of the residual alike, dweight float32 [cols])."""
+    shape = dy.shape if isinstance(dy, torch.Tensor) else None
+    dy2 = _rows(dy, "dy", None)
+    dev = dy2.device
+    rows, cols = dy2.shape
+    if cols % 8:
+        raise ValueError(f"dy must have a multiple of 8 columns, not {cols}")
+    h2 = _rows(h, "h", shape, dev)
+    weight = _norm_weight(weight, cols, dev)
+    _need(rstd, "rstd", torch.float32, dev)
+    if tuple(rstd.shape) != (rows,):
+        raise ValueError(f"rstd must be [{rows}]")
+    rstd = rstd.contiguous()
+    dh2 = None if dh is None else _rows(dh, "dh", shape, dev)
+    dx = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    dweight = torch.empty((cols,), dtype=torch.float32, device=dev)
+    nbytes = (_mxq._lib or _mxq.load()).mxq_rmsnorm_backward_workspace_size(rows, cols)
+    ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
+    _call("mxq_rmsnorm_backward", dev, _RMSNORM_BACKWARD.pack(
+        dy2.data_ptr(), h2.data_ptr(), 0 if dh2 is None else dh2.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
+        dx.data_ptr(), dweight.data_ptr(), 0 if ws is None else ws.data_ptr(), nbytes, rows, cols, dy2.stride(0),
+        h2.stride(0), 0 if dh2 is None else dh2.stride(0), weight.dtype is torch.float32, 0))
+    return dx, dweight

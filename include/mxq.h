@@ -489,6 +489,72 @@ mxq_status nvfp4_matvec(const uint16_t *x, int64_t tokens, int64_t ldx, const ui
                         int64_t ldy, int out_fp32, void *stream);
 
 /*
+ * RMS norm with the residual's addition and an output in 8 bits:
+ *   h = bf16_RNE(x + residual) (x itself without one),
+ *   r = 1 / sqrt(mean(h^2) + eps),  y = h * r * weight  in fp32,
+ * and y quantized as it stands, as blockfp8_quantize_1x128 (blockfp8_rmsnorm) or
+ * mxq_quantize_rowwise (mxq_rmsnorm) quantize, except that y is not rounded to
+ * bf16 before.
+ *   x, residual  [rows, cols] bf16, row strides in elements (multiples of 8);
+ *           residual may be NULL
+ *   weight  [cols] bf16, or fp32 when weight_fp32 != 0
+ *   q       [rows, cols] codes, contiguous, 8-byte aligned
+ *   scale   fp32 [rows, ceil(cols/128)], or E8M0 [rows, cols/32], contiguous
+ *   h       [rows, cols] bf16, contiguous; needed with a residual, else optional;
+ *           may be x or residual where those are contiguous
+ *   y       optional [rows, cols] bf16: y rounded (for a column-wise quantizer)
+ *   rstd    optional fp32 [rows]: r
+ * x, residual, weight, h and y are 16-byte aligned.  Shape: cols a multiple of 8
+ * (blockfp8) or 32, at most 16384 (MXQ_ESIZE).  The sum of squares is fp32: values
+ * over 2^63 / sqrt(cols) make it infinite, and y zero.
+ */
+typedef struct mxq_rmsnorm_args {
+    const uint16_t *x, *residual;
+    const void *weight;
+    uint8_t *q;
+    void *scale;
+    uint16_t *h, *y;
+    float *rstd;
+    int64_t rows, cols, ldx, ld_residual;
+    float eps;
+    int32_t weight_fp32;
+    int64_t reserved; /* set to 0 */
+} mxq_rmsnorm_args;
+
+mxq_status blockfp8_rmsnorm(const mxq_rmsnorm_args *args, void *stream);
+mxq_status mxq_rmsnorm(const mxq_rmsnorm_args *args, void *stream);
+
+/*
+ * The gradient of that norm, the quantizer counted as the identity: with u = h * r
+ * and g = dy * weight,
+ *   dx = bf16_RNE(r * (g - u * mean(g * u)) + dh),  dweight = sum over rows of dy * u
+ *   dy, h, dh  [rows, cols] bf16, row strides in elements (multiples of 8); dh, the
+ *           gradient that reaches h past the norm, may be NULL; 16-byte aligned
+ *   rstd    fp32 [rows] as the norm wrote it
+ *   dx      [rows, cols] bf16, contiguous, the gradient of x and of residual; may
+ *           be dy, dh or h where those are contiguous
+ *   dweight fp32 [cols]; zeros for no rows
+ *   workspace  >= mxq_rmsnorm_backward_workspace_size(rows, cols) bytes, 16-byte
+ *           aligned, no initial contents needed; may be NULL when that is 0
+ * Shape: cols a multiple of 8, at most 16384.  Equal calls give equal bytes.
+ */
+typedef struct mxq_rmsnorm_backward_args {
+    const uint16_t *dy, *h, *dh;
+    const void *weight;
+    const float *rstd;
+    uint16_t *dx;
+    float *dweight;
+    void *workspace;
+    size_t workspace_bytes;
+    int64_t rows, cols, ld_dy, ldh, ld_dh;
+    int32_t weight_fp32;
+    int32_t reserved; /* set to 0 */
+} mxq_rmsnorm_backward_args;
+
+size_t mxq_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols);
+mxq_status mxq_rmsnorm_backward(const mxq_rmsnorm_backward_args *args, void *stream);
+
+/*
  * Products of 8-bit tokens with 8-bit weights (blockfp8_*: block-FP8, mxq_*:
  * MXFP8), summed in fp32, rounded once:
  *   y[i, j] = sum_k x[i, k] w[j, k]
