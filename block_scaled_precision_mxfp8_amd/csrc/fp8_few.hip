@@ -47,13 +47,13 @@ __global__ __launch_bounds__(W * 64) void few_kernel(Fp8Matmul a)
     const uint8_t *x = a.x + (int64_t)row0 * a.ldx;
     const uint8_t *w = a.w + (kRagged == kRows ? group * a.w_stride : 0) + (int64_t)col0 * a.ldw;
     const int xlast = row_end - row0 - 1, wlast = col_end - col0 - 1;  // rows past them repeat them
-    const uint32_t chunk = (lane & 7) ^ (lane >> 3);  // as in fp8_tiles.hip
+    const uint32_t chunk = (lane & 7) ^ (lane >> 4);  // as in fp8_tiles.hip
     uint32_t voff[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
         const int r = i * 8 + (lane >> 3);
         voff[i] = (i < 2 * R ? (uint32_t)min(r, wlast) * (uint32_t)a.ldw
-                             : (uint32_t)min(r - R * 16, xlast) * (uint32_t)a.ldx) + chunk * 16;
+                             : (uint32_t)min(r - R * 16, xlast) * (uint32_t)a.ldx) + (chunk ^ (i & 1) * 4) * 16;
     }
     const __amdgpu_buffer_rsrc_t wr = buffer_at(w), xr = buffer_at(x);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
@@ -61,10 +61,11 @@ __global__ __launch_bounds__(W * 64) void few_kernel(Fp8Matmul a)
         const uint32_t to = (wave * D + (s - s0) % D) * kSlot;
         const uint32_t from = (uint32_t)s * kStep;
         // k % 16 == 0; what lies past it is zero
-        const uint32_t past = (int32_t)(from + chunk * 16) < a.k ? 0u : kNowhere;
+        const uint32_t past[2] = {(int32_t)(from + chunk * 16) < a.k ? 0u : kNowhere,
+                                  (int32_t)(from + (chunk ^ 4) * 16) < a.k ? 0u : kNowhere};
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            load_to_lds(i < 2 * R ? wr : xr, lds0 + to + i * 1024, voff[i] | past, from);
+            load_to_lds(i < 2 * R ? wr : xr, lds0 + to + i * 1024, voff[i] | past[i & 1], from);
     };
 
     // -- scales of kScaleSteps steps from s on: lane (p, g) has row p's of steps 4 g ..
@@ -92,7 +93,7 @@ __global__ __launch_bounds__(W * 64) void few_kernel(Fp8Matmul a)
 #pragma unroll
         for (int t = 0; t < T; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int at0 = p * kStep + ((g ^ (p & 7)) << 4), at1 = p * kStep + (((g + 4) ^ (p & 7)) << 4);
+    const int at0 = p * kStep + ((g ^ (p >> 1)) << 4), at1 = p * kStep + (((g + 4) ^ (p >> 1)) << 4);
     auto step = [&](int32_t s, auto J) {  // step s, in place J of four of its lane group
         constexpr int j = J;
         const int from = ((s - s0) % kScaleSteps / 4) * 16 + p;  // the lane that has its scales

@@ -26,15 +26,20 @@ namespace {
 struct TileGrid {
     int32_t tm, tn;  // tiles of rows (at most, if grouped) and of columns
     int32_t sm, sn;  // tiles of a block that one XCD works on at a time
-    int32_t bm;      // such blocks down
+    int32_t bm, bn;  // such blocks
+    int32_t groups;  // that each have all tiles (kContraction, else 1)
 };
 
 // A block of sm x sn tiles, as many as an XCD has CUs, shares its rows and columns
-// in that XCD's L2.  Workgroup i runs on XCD i % 8.
-__device__ __forceinline__ bool tile_of(const TileGrid &g, int32_t &tm, int32_t &tn)
+// in that XCD's L2.  Workgroup i runs on XCD i % 8.  With several groups, which may
+// differ much in length, every XCD gets as many blocks of each, and the XCDs begin
+// with different ones.
+__device__ __forceinline__ bool tile_of(const TileGrid &g, int32_t &tm, int32_t &tn, int32_t &group)
 {
     const int32_t xcd = blockIdx.x % 8, local = blockIdx.x / 8, each = g.sm * g.sn;
-    const int32_t block = local / each * 8 + xcd, in = local % each;
+    const int32_t in = local % each, turn = local / each;
+    group = (turn + xcd * (g.groups / 8)) % g.groups;
+    const int32_t block = turn / g.groups * 8 + (xcd + group) % 8;
     tm = block % g.bm * g.sm + in % g.sm;
     tn = block / g.bm * g.sn + in / g.sm;
     return tm < g.tm && tn < g.tn;
@@ -52,14 +57,12 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
     __shared__ __align__(1024) uint8_t lds[2 * kStage];
     __shared__ __align__(16) uint32_t scales[3][4][kScaled];
 
-    int32_t tm, tn;
-    if (!tile_of(grid, tm, tn)) return;
-    int group = 0;
+    int32_t tm, tn, group;
+    if (!tile_of(grid, tm, tn, group)) return;
     int32_t row0 = tm * BM, row_end = min(row0 + BM, a.m), k0 = 0, k1 = a.k;
     if constexpr (kRagged == kRows) {
         if (!find_row_tile(a, BM, tm, group, row0, row_end)) return;
     } else if constexpr (kRagged == kContraction) {
-        group = blockIdx.y;
         k0 = k_offset_at(a, group);
         k1 = max(k0, k_offset_at(a, group + 1));
     }
@@ -79,37 +82,41 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
                                : a.w + (kRagged == kRows ? group * a.w_stride : 0) +
                                      (int64_t)col0 * a.ldw;
     const int last = (of_x ? row_end - row0 : col_end - col0) - 1;  // rows past it repeat it: their results are dropped
-    // Row r's 16-byte piece c lies at piece c ^ (r % 8) of its line in LDS: eight
-    // rows' pieces of one c, read together, then fall on all banks.
-    const uint32_t chunk = (lane & 7) ^ (lane >> 3);
-    uint32_t vrow = (lane >> 3) * (uint32_t)ld;
-    auto rows_at = [&](int i) { return (uint32_t)min(first + i * 8, last) * (uint32_t)ld; };
-    auto in_rows = [&](int i) {
-        return min(vrow, (uint32_t)__builtin_amdgcn_readfirstlane(max(min(last - first - i * 8, 7), 0) * (int)ld)) +
-               chunk * 16;
-    };
+    // Row r's 16-byte piece c lies at piece c ^ (r / 2 % 8) of its line in LDS: sixteen
+    // rows' pieces of one c, read together, then fall on all 64 banks.  (c ^ (r % 8), for
+    // 32 banks, leaves two on each: block-FP8 8192 x 8192 x 7168 took 5 % longer.)
+    const uint32_t chunk = (lane & 7) ^ (lane >> 4);  // in even loads; odd ones are four rows on: chunk ^ 4
+    const uint32_t vrow = (lane >> 3) * (uint32_t)ld;
     const __amdgpu_buffer_rsrc_t rsrc = buffer_at(base);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
+    // The i-th load of step s; a step past the last one's reads nothing.
+    uint32_t piece_at[2];
+    auto aim = [&](int32_t s) {  // what lies past the contraction's end is zero
+        const int left = k1 - k0 - s * kStep - 16;
+        piece_at[0] = chunk * 16 | ((int)(chunk * 16) > left ? kNowhere : 0u);
+        piece_at[1] = (chunk ^ 4) * 16 | ((int)((chunk ^ 4) * 16) > left ? kNowhere : 0u);
+    };
+    auto fill_one = [&](int32_t s, int i) {
+        const int r = first + i * 8;
+        const uint32_t in_rows = min(vrow, (uint32_t)__builtin_amdgcn_readfirstlane(max(min(last - r, 7), 0) * (int)ld));
+        load_to_lds(rsrc, lds0 + (s & 1) * kStage + (wave * kLoads + i) * 1024, in_rows + piece_at[i & 1],
+                    __builtin_amdgcn_readfirstlane(min(r, last) * (int)ld + k0 + s * kStep));
+    };
     auto fill = [&](int32_t s) {
-        const uint32_t to = (s & 1) * kStage + wave * kLoads * 1024;
-        const uint32_t from = (uint32_t)(k0 + s * kStep);
-        const int have = k1 - k0 - s * kStep - (int32_t)chunk * 16;
-        if (kRagged != kContraction || s < full || (k1 & 15) == 0) {
-            asm volatile("" : "+v"(vrow));  // eight addresses made anew take less than eight registers kept
-            const uint32_t past = have < 16 ? kNowhere : 0u;  // what lies past the contraction's end is zero
+        aim(s);
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                load_to_lds(rsrc, lds0 + to + i * 1024, in_rows(i) | past,
-                            __builtin_amdgcn_readfirstlane(rows_at(i) + from));
-        } else {  // it ends inside 16 bytes
-#pragma unroll 1
-            for (int i = 0; i < kLoads; ++i) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                const uint8_t *q = base + (size_t)(rows_at(i) + in_rows(i)) + from;
-                if (have >= 16) v = *reinterpret_cast<const uint4 *>(q);
-                else if (have > 0) v = first_bytes(q, have);
-                *reinterpret_cast<uint4 *>(lds + to + i * 1024 + lane * 16) = v;
-            }
+        for (int i = 0; i < kLoads; ++i) fill_one(s, i);
+    };
+    // Where the contraction ends inside 16 bytes, these are put in place by hand once
+    // the last step is there otherwise.
+    auto finish = [&](int32_t s) {
+        if (kRagged == kContraction && (k1 & 15) != 0 && s == steps - 1) {
+            const int at = (k1 - k0) % kStep & ~15;
+            const int r = tid < BM ? tid : tid - BM;
+            const uint8_t *row = tid < BM ? a.x + (int64_t)(row0 + min(r, row_end - row0 - 1)) * a.ldx
+                                          : a.w + (int64_t)(col0 + min(r, col_end - col0 - 1)) * a.ldw;
+            *reinterpret_cast<uint4 *>(lds + (s & 1) * kStage + tid * kStep + (((at >> 4) ^ (r >> 1 & 7)) << 4)) =
+                first_bytes(row + (k1 & ~15), k1 & 15);
         }
     };
 
@@ -162,7 +169,7 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
     // -- operands: four places of a row's line, by the half of the step and of the operand
     uint32_t at[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) at[i] = p * kStep + (((2 * i + h) ^ (p & 7)) << 4);
+    for (int i = 0; i < 4; ++i) at[i] = p * kStep + (((2 * i + h) ^ (p >> 1 & 7)) << 4);
     auto operand = [&](uint32_t stage, int row, int t) {  // rows row .., half t
         const uint8_t *q = lds + stage + row * kStep;
         return join(*reinterpret_cast<const uint4 *>(q + at[2 * t]),
@@ -192,11 +199,11 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
     auto turn = [&](int32_t s) {
         settle();
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        const bool scales_due = (s + 1) % 4 == 0 && (s + 1) / 4 < last_group;
-        if (scales_due) store_scales((s + 1) / 4 & 1);
+        finish(s + 1);
+        if ((s + 1) % 4 == 0 && (s + 1) / 4 < last_group) store_scales((s + 1) / 4 & 1);
         __syncthreads();
         if ((s + 1) % 4 == 0 && (s + 1) / 4 + 1 < last_group) load_scales((s + 1) / 4 + 1);
-        if (s + 2 < steps) fill(s + 2);
+        aim(s + 2);
     };
     if (steps > 0) {
         fill(0);
@@ -206,10 +213,15 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
             load_scales(0);
             store_scales(0);
         }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
         if (1 < last_group) load_scales(1);
-        if (1 < steps) fill(1);
+        if (1 < steps) {
+            fill(1);
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        finish(0);
+        __syncthreads();
     }
     if constexpr (kExact) {
         for (int32_t s = 0; s < steps; ++s) {
@@ -271,6 +283,8 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
                 }
             }
             turn(s);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) fill_one(s + 2, i);
         }
     } else if constexpr (kMX) {
         i32x8 b0[CT], b1[CT], w[RT];
@@ -301,6 +315,7 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
                 for (int c = 0; c < CT; ++c)
                     acc[r][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                         w[r], b0[c], acc[r][c], 0, 0, 0, sr[r], 0, sx[c]);
+                __builtin_amdgcn_sched_barrier(0);  // into the same registers
                 fetch_w(r, s, 1);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -313,7 +328,11 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
                 for (int c = 0; c < CT; ++c)
                     acc[r][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                         w[r], b1[c], acc[r][c], 0, 0, 2, sr[r], 2, sx[c]);
+                __builtin_amdgcn_sched_barrier(0);
                 fetch_w(r, s + 1, 0);
+                // between products, not in a row: each of these holds the wave up
+#pragma unroll
+                for (int i = 0; i < kLoads / RT; ++i) fill_one(s + 2, r * (kLoads / RT) + i);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -343,54 +362,63 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
                     for (int i = 0; i < 16; ++i)
                         acc[r][c][i] = __builtin_fmaf(q[i], f[c], acc[r][c][i]);
                 }
+                if (r == 0) aim(s + 1);
+                if (s > 0) {
+#pragma unroll
+                    for (int i = 0; i < kLoads / RT; ++i) fill_one(s + 1, r * (kLoads / RT) + i);
+                }
             }
             turn(s);
         }
     }
 
-    // -- out: a wave turns 32 tokens at a time around in LDS and writes their rows
+    // -- out (what is still on its way to LDS, nothing but zeros, is let in first): a wave turns 32 tokens at a time around in 8 KiB of LDS and writes rows of
+    // 256 bytes, 16 a lane: bf16 for a wave's 128 columns (64 in the small tiles), fp32
+    // for 64.  Piece j of row r, two lanes' worth, lies at j ^ (r % 8).
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    // four neighbouring floats c / 4 of row r at place (c / 4) ^ (r % 8) of it: no bank
-    // is hit twice by eight rows
-    constexpr int kCols = RT * 32;
-    static_assert(kWaves * 32 * kCols * 4 <= 2 * kStage, "fits the stages");
-    float *out = reinterpret_cast<float *>(lds) + wave * 32 * kCols;
-    auto place = [&](int r, int c) { return out + r * kCols + (((c >> 2) ^ (r & 7)) << 2) + (c & 3); };
+    constexpr int kCols = RT * 32, kSize = kExact ? 4 : 2, kRow = kCols * kSize;
+    constexpr int kPieces = kRow / 16, kRowsAt = 64 / kPieces;  // pieces of a row, rows that 64 lanes write
+    static_assert(kPieces >= 8 && kPieces <= 64 && kWaves * 32 * kRow <= 2 * kStage, "fits the stages");
+    uint8_t *mine = lds + wave * 32 * kRow;
     const int wcol = col0 + wn * kCols, cols = min(kCols, col_end - wcol);
-    const bool f32 = a.out_f32 != 0;
-    const int size = f32 ? 4 : 2;
-    uint8_t *y = static_cast<uint8_t *>(a.y) + (kRagged == kContraction ? group * a.y_stride * size : 0);
-    const bool wide = cols == kCols && (reinterpret_cast<uintptr_t>(y) & 15) == 0 && a.ldy * size % 16 == 0;
+    uint8_t *y = static_cast<uint8_t *>(a.y) + (kRagged == kContraction ? group * a.y_stride * kSize : 0);
+    const bool wide = cols == kCols && (reinterpret_cast<uintptr_t>(y) & 15) == 0 && a.ldy * kSize % 16 == 0;
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<f32x4 *>(place(p, r * 32 + 8 * i + 4 * h)) =
-                    f32x4{acc[r][c][4 * i], acc[r][c][4 * i + 1], acc[r][c][4 * i + 2], acc[r][c][4 * i + 3]};
+            for (int i = 0; i < 4; ++i) {
+                const int byte = (r * 32 + 8 * i + 4 * h) * kSize;
+                uint8_t *to = mine + p * kRow + (((byte >> 4) ^ (p & 7)) << 4) + (byte & 15);
+                const f32x16 &v = acc[r][c];
+                if constexpr (kExact)
+                    *reinterpret_cast<f32x4 *>(to) = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+                else
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(bf16x2_rne(v[4 * i], v[4 * i + 1]),
+                                                                bf16x2_rne(v[4 * i + 2], v[4 * i + 3]));
+            }
         __builtin_amdgcn_wave_barrier();
         const int32_t trow = row0 + (wt * CT + c) * 32;
         const int rows = min(32, row_end - trow);
         if (wide) {
-            constexpr int kPer = kCols / 4;  // lanes on a row
 #pragma unroll
-            for (int i = 0; i < 32 * kPer / 64; ++i) {
-                const int e = i * 64 + lane, tr = e / kPer, tc = e % kPer * 4;
-                if (tr < rows) {
-                    const f32x4 v = *reinterpret_cast<const f32x4 *>(place(tr, tc));
-                    const int64_t to = (int64_t)(trow + tr) * a.ldy + wcol + tc;
-                    if (f32)
-                        *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(y) + to) = v;
-                    else
-                        *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(y) + to) =
-                            make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
-                }
+            for (int i = 0; i < 32 / kRowsAt; ++i) {
+                const int tr = i * kRowsAt + lane / kPieces, j = lane % kPieces;
+                const uint4 v = *reinterpret_cast<const uint4 *>(mine + tr * kRow + ((j ^ (tr & 7)) << 4));
+                if (tr < rows)
+                    *reinterpret_cast<uint4 *>(y + ((int64_t)(trow + tr) * a.ldy + wcol) * kSize + j * 16) = v;
             }
         } else if (cols > 0) {
             for (int tr = 0; tr < rows; ++tr)
-                for (int tc = lane; tc < cols; tc += 64)
-                    store_product(y, (int64_t)(trow + tr) * a.ldy + wcol + tc, *place(tr, tc), f32);
+                for (int tc = lane; tc < cols; tc += 64) {
+                    const int byte = tc * kSize;
+                    const uint8_t *from = mine + tr * kRow + (((byte >> 4) ^ (tr & 7)) << 4) + (byte & 15);
+                    uint8_t *to = y + ((int64_t)(trow + tr) * a.ldy + wcol + tc) * kSize;
+                    if constexpr (kExact) *reinterpret_cast<uint32_t *>(to) = *reinterpret_cast<const uint32_t *>(from);
+                    else *reinterpret_cast<uint16_t *>(to) = *reinterpret_cast<const uint16_t *>(from);
+                }
         }
         __builtin_amdgcn_wave_barrier();
     }
@@ -405,13 +433,15 @@ hipError_t launch(const Fp8Matmul &a, hipStream_t stream)
     g.tn = (a.n + BN - 1) / BN;
     g.sm = g.tm < 8 ? g.tm : 8;
     g.sn = 32 / g.sm < g.tn ? 32 / g.sm : g.tn;
+    if (kRagged == kContraction)  // every group's blocks are dealt to eight XCDs anew: smaller ones come out even
+        while (g.sm * g.sn > 8) (g.sm > g.sn ? g.sm : g.sn) /= 2;
     g.bm = (g.tm + g.sm - 1) / g.sm;
-    const int64_t blocks = (int64_t)g.bm * ((g.tn + g.sn - 1) / g.sn);
-    const int64_t wgs = (blocks + 7) / 8 * 8 * g.sm * g.sn;
-    const int64_t groups = kRagged == kContraction ? a.groups : 1;
-    if (wgs > 0x7FFFFFFF || groups > 65535) return hipErrorInvalidConfiguration;
+    g.bn = (g.tn + g.sn - 1) / g.sn;
+    g.groups = kRagged == kContraction ? a.groups : 1;
+    const int64_t wgs = ((int64_t)g.bm * g.bn + 7) / 8 * 8 * g.sm * g.sn * g.groups;
+    if (wgs > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
     tile_kernel<kMX, kExact, kRagged, WT, WN, CT, RT>
-        <<<dim3((unsigned)wgs, (unsigned)groups), dim3(WT * WN * 64), 0, stream>>>(a, g);
+        <<<dim3((unsigned)wgs), dim3(WT * WN * 64), 0, stream>>>(a, g);
     return hipGetLastError();
 }
 
@@ -420,7 +450,7 @@ hipError_t pick(const Fp8Matmul &a, hipStream_t stream)
 {
     if (a.out_f32) return launch<kMX, true, kRagged, 2, 2, 2, 2>(a, stream);
     const int64_t big = (int64_t)((a.m + 255) / 256) * ((a.n + 255) / 256) * (kRagged == kContraction ? a.groups : 1);
-    if (big >= 128 && kRagged != kContraction) return launch<kMX, false, kRagged, 4, 2, 2, 4>(a, stream);
+    if (big >= 128) return launch<kMX, false, kRagged, 4, 2, 2, 4>(a, stream);
     return launch<kMX, false, kRagged, 2, 2, 2, 2>(a, stream);
 }
 
