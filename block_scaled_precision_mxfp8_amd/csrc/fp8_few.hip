@@ -210,14 +210,36 @@ hipError_t launch(const Fp8Matmul &a, hipStream_t stream)
     return hipGetLastError();
 }
 
+// Rows to a workgroup (R x 16) so that every CU has one and none has a second turn for
+// a few rows; with few rows more waves cut the contraction, and two workgroups fit a CU
+// where LDS allows.  us for n x k = 4096 x 7168, 8192 x 8192, 16384 x 7168 on MI355X:
+//   tokens      R 1, 8 waves         R 2, 4 waves         R 4, 4 waves
+//     8 .. 16   7.1 13.3 25          8.1 13.5 23          11.3 13.5 23
+//    32         8.2 15.8 38          10.6 13.8 26         14.7  -   25
+//    64        12.0 23.3 52          15.1 17.5 38         23.2 25.6 30
+// (T one less than needed for 33 x 4097: 257 workgroups of 16 rows 16.0, 129 of 32 12.6.)
+template <bool kMX, int kRagged, int T>
+hipError_t pick_rows(const Fp8Matmul &a, hipStream_t stream)
+{
+    const int64_t at_once = (int64_t)a.n * (kRagged == kRows ? a.groups : 1);
+    if (at_once <= 16 * 256) return launch<kMX, kRagged, 1, T, 8, 2>(a, stream);
+    if (T == 1 || at_once <= 32 * 256 || kRagged == kRows)
+        return launch<kMX, kRagged, 2, T, 4, T == 1 ? 3 : 2>(a, stream);
+    return launch<kMX, kRagged, 4, T, 4, 2>(a, stream);
+}
+
 template <bool kMX, int kRagged>
 hipError_t pick(const Fp8Matmul &a, int tokens, hipStream_t stream)
 {
-    if (tokens <= 16)
-        return a.n <= 8192 ? launch<kMX, kRagged, 1, 1, 8, 4>(a, stream) : launch<kMX, kRagged, 2, 1, 8, 3>(a, stream);
-    if (tokens <= 32)
-        return a.n <= 8192 ? launch<kMX, kRagged, 1, 2, 8, 3>(a, stream) : launch<kMX, kRagged, 2, 2, 4, 4>(a, stream);
-    return a.n <= 8192 ? launch<kMX, kRagged, 1, 4, 4, 3>(a, stream) : launch<kMX, kRagged, 2, 4, 4, 3>(a, stream);
+    if constexpr (kRagged == kRows) {
+        // 512 rows of 128 groups: T 1 294 us, 2 292; longer groups take more tiles
+        return tokens <= 16 ? pick_rows<kMX, kRagged, 2>(a, stream) : pick_rows<kMX, kRagged, 4>(a, stream);
+    } else {
+        if (tokens <= 16) return pick_rows<kMX, kRagged, 1>(a, stream);
+        if (tokens <= 32) return pick_rows<kMX, kRagged, 2>(a, stream);
+        if (tokens <= 48) return pick_rows<kMX, kRagged, 3>(a, stream);
+        return pick_rows<kMX, kRagged, 4>(a, stream);
+    }
 }
 
 }  // namespace

@@ -102,7 +102,7 @@ hipError_t launch_fp4_matvec(bool nv, const uint16_t *x, int64_t tokens, int64_t
 // Products with 8-bit operands (fp8_matmul.hpp); ragged: a Ragged.
 struct Fp8Matmul;
 hipError_t launch_fp8_matmul(bool mx, int ragged, const Fp8Matmul &a, hipStream_t stream);
-// for up to 64 tokens, or about as many in a group
+// for few tokens (of one group, on average, if grouped)
 hipError_t launch_fp8_few(bool mx, int ragged, int tokens, const Fp8Matmul &a, hipStream_t stream);
 
 // RMS norm with 8-bit output, and its gradient; every output but q, scale, dx and

@@ -8,8 +8,8 @@
 // rounded to bf16 first, so codes can differ from those of a separate norm and
 // quantizer by that rounding.  Gradient, u = h * r, g = dy * weight:
 //   dx = r * (g - u * mean(g * u)) + dh,  dweight = sum over the rows of dy * u
-// (the quantizer counts as the identity).  Sums are fp32, of 8 values in a lane, then
-// over lanes and waves in a fixed order.
+// (the quantizer counts as the identity).  Sums are of 8 values of a lane in fp32, then
+// over lanes and waves in a fixed order, in fp64 for the norm and fp32 for the gradient.
 
 #include "launch.hpp"
 #include "mxq_device.hpp"
@@ -50,8 +50,8 @@ __device__ __forceinline__ Row8 weights8(const void *w, int64_t col)
 
 // Sum over the kWaves waves of a row, the same in all of them.  `slot` alternates so
 // that one barrier a sum is enough.
-template <int kWaves>
-__device__ __forceinline__ float row_sum(float v, float (*red)[8], int slot)
+template <int kWaves, class F>
+__device__ __forceinline__ F row_sum(F v, F (*red)[8], int slot)
 {
 #pragma unroll
     for (int off = 1; off < kWave; off <<= 1) v += __shfl_xor(v, off, kWave);
@@ -65,6 +65,14 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[8], int slot)
         for (int i = 1; i < kWaves; ++i) v += red[slot][first + i];
     }
     return v;
+}
+
+// v^-1/2 in 64 bits: a Newton step from the 32-bit approximation doubles its bits.
+__device__ __forceinline__ double inverse_root(double v)
+{
+    if (!(v >= 0x1p-100 && v <= 0x1p100)) return 1.0 / __builtin_sqrt(v);
+    const double y = __builtin_amdgcn_rsqf((float)v);
+    return y * __builtin_fma(-0.5 * v * y, y, 1.5);
 }
 
 // Largest magnitude's bits over groups of 16 lanes.
@@ -88,12 +96,12 @@ template <bool kMX, int kWaves, bool kWeightF32>
 __global__ __launch_bounds__(kWaves < 4 ? 256 : kWaves * 64) void rmsnorm_kernel(RmsNorm a)
 {
     constexpr int kThreads = kWaves < 4 ? 256 : kWaves * 64, kRows = kThreads / (kWaves * 64);
-    __shared__ float red[1][8];
+    __shared__ double red[1][8];
     const int in_row = threadIdx.x % (kWaves * 64);
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / (kWaves * 64);
     const bool live = row < a.rows;
     uint4 v[kVecs];
-    float sum = 0.f;
+    double sum = 0;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         const int64_t col = (int64_t)(i * kWaves * 64 + in_row) * 8;
@@ -119,8 +127,10 @@ __global__ __launch_bounds__(kWaves < 4 ? 256 : kWaves * 64) void rmsnorm_kernel
         for (int j = 0; j < 8; ++j) s = __builtin_fmaf(f.f[j], f.f[j], s);
         sum += s;
     }
-    sum = row_sum<kWaves>(sum, red, 0);
-    const float r = 1.0f / __builtin_sqrtf(sum / (float)a.cols + a.eps);
+    // r is held in two floats and r * weight too: y is rounded about once, so that few
+    // codes and hardly a scale fall to the other side of a border.
+    const double root = inverse_root(row_sum<kWaves>(sum, red, 0) / (double)a.cols + (double)a.eps);
+    const float r = (float)root, r_low = r < __builtin_inff() ? (float)(root - (double)r) : 0.f;
     if (a.rstd && live && in_row == 0) a.rstd[row] = r;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
@@ -132,7 +142,10 @@ __global__ __launch_bounds__(kWaves < 4 ? 256 : kWaves * 64) void rmsnorm_kernel
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            y.f[j] = y.f[j] * r * w.f[j];
+            const float t = r * w.f[j];
+            const float low = __builtin_fabsf(t) < __builtin_inff()
+                                  ? __builtin_fmaf(r, w.f[j], -t) + r_low * w.f[j] : 0.f;
+            y.f[j] = __builtin_fmaf(y.f[j], t, y.f[j] * low);
             if (!in) y.f[j] = 0.f;
             m = max(m, __float_as_uint(y.f[j]) & 0x7FFFFFFFu);
         }

@@ -14,7 +14,7 @@ import struct
 import torch
 
 import block_scaled_precision_mxfp8_amd as _mxq
-from .decode import _as_bytes, _need, _stream_of
+from .decode import _need, _stream_of
 
 # mxq_matmul_args, mxq_rmsnorm_args and mxq_rmsnorm_backward_args as bytes: packing
 # them costs a fraction of filling a ctypes structure field by field
@@ -22,11 +22,13 @@ _MATMUL = struct.Struct("@PPqqPPqqqqPqqPqqqiiq")
 _RMSNORM = struct.Struct("@PPPPPPPPqqqqfiq")
 _RMSNORM_BACKWARD = struct.Struct("@PPPPPPPPNqqqqqii")
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
 
 def _call(fn: str, device: torch.device, args: bytes):
     """One library call on the current stream of ``device``, made current where it is not."""
     f = getattr(_mxq._lib or _mxq.load(), fn)
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         st = f(args, _stream_of(device))
     else:
         with torch.cuda.device(device):
@@ -36,33 +38,36 @@ def _call(fn: str, device: torch.device, args: bytes):
 
 
 def _codes(t, what: str, dims: int, device=None) -> torch.Tensor:
-    """E4M3 codes as uint8 with a unit last stride and 16-byte aligned rows (a copy if they have none)."""
-    t = _as_bytes(t, what)
+    """E4M3 codes with a unit last stride and 16-byte aligned rows (a copy if they have none)."""
+    if not isinstance(t, torch.Tensor) or (t.dtype is not torch.uint8 and t.dtype is not torch.float8_e4m3fn):
+        raise TypeError(f"{what} must be a uint8 or float8_e4m3fn tensor")
     if device is None:
         if not t.is_cuda:
             raise ValueError(f"{what} must live on the GPU (the library has no CPU path)")
     elif t.device != device:
         raise ValueError(f"{what} must be on {device}")
-    if t.dim() != dims:
+    stride = t.stride()
+    if len(stride) != dims:
         raise ValueError(f"{what} must have {dims} dimensions")
-    *rows, unit = t.stride()
-    if unit != 1 or t.data_ptr() % 16 or rows[-1] < t.shape[-1] or any(v % 16 for v in rows):
-        if t.shape[-1] % 16 == 0:
-            return t.clone(memory_format=torch.contiguous_format)
-        # rows of their own, apart by a multiple of 16 bytes
-        wide = t.new_empty((*t.shape[:-1], (t.shape[-1] + 15) // 16 * 16))[..., :t.shape[-1]]
-        return wide.copy_(t)
-    return t
+    if stride[-1] == 1 and not t.data_ptr() & 15 and not stride[-2] & 15 and stride[-2] >= t.shape[-1] \
+            and (dims == 2 or not stride[0] & 15):
+        return t
+    if t.shape[-1] % 16 == 0:
+        return t.clone(memory_format=torch.contiguous_format)
+    # rows of their own, apart by a multiple of 16 bytes
+    wide = t.new_empty((*t.shape[:-1], (t.shape[-1] + 15) // 16 * 16))[..., :t.shape[-1]]
+    return wide.copy_(t)
 
 
-def _scales(t, what: str, shape, mx: bool, device) -> torch.Tensor:
+def _scales(t, what: str, shape: tuple, mx: bool, device) -> torch.Tensor:
     if mx:
-        t = _as_bytes(t, what)
+        if not isinstance(t, torch.Tensor) or (t.dtype is not torch.uint8 and t.dtype is not torch.float8_e8m0fnu):
+            raise TypeError(f"{what} must be a uint8 or float8_e8m0fnu tensor")
         if t.device != device:
             raise ValueError(f"{what} must be on {device}")
     else:
         _need(t, what, torch.float32, device)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)}, not {list(t.shape)}")
     stride = t.stride()
     if stride[-1] != 1 or stride[-2] < shape[-1]:
@@ -70,13 +75,13 @@ def _scales(t, what: str, shape, mx: bool, device) -> torch.Tensor:
     return t
 
 
-def _out(out, shape, dtype, device) -> torch.Tensor:
+def _out(out, shape: tuple, dtype, like: torch.Tensor) -> torch.Tensor:
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError("out_dtype must be bfloat16 or float32")
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(out, "out", dtype, device)
-    if tuple(out.shape) != tuple(shape) or not out.is_contiguous():
+        return like.new_empty(shape, dtype=dtype)
+    _need(out, "out", dtype, like.device)
+    if out.shape != shape or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {list(shape)} tensor")
     return out
 
@@ -88,8 +93,8 @@ def _offsets(offsets, device) -> torch.Tensor:
     return offsets.contiguous()
 
 
-def _launch(fn: str, x, sx, w, sw, y, n: int, k: int, offsets=None, w_stride=0, sw_stride=0, y_stride=0):
-    _call(fn, x.device, _MATMUL.pack(
+def _launch(fn: str, dev, x, sx, w, sw, y, n: int, k: int, offsets=None, w_stride=0, sw_stride=0, y_stride=0):
+    _call(fn, dev, _MATMUL.pack(
         x.data_ptr(), sx.data_ptr(), x.stride(0), sx.stride(0), w.data_ptr(), sw.data_ptr(),
         w.stride(-2), sw.stride(-2), w_stride, sw_stride, y.data_ptr(), n, y_stride,
         0 if offsets is None else offsets.data_ptr(), x.shape[0], n, k,
@@ -102,22 +107,21 @@ def _matmul(fn: str, mx: bool, q, s, wq, ws, out_dtype, out, offsets=None) -> to
     dev = q.device
     wq = _codes(wq, "wq", 2 if offsets is None else 3, dev)
     m, k = q.shape
-    n = wq.shape[-2]
-    if wq.shape[-1] != k:
-        raise ValueError(f"q has {k} columns, the weights {wq.shape[-1]}")
+    *lead, n, wk = wq.shape
+    if wk != k:
+        raise ValueError(f"q has {k} columns, the weights {wk}")
     step, size = (32, 32) if mx else (16, 128)
     if k % step:
         raise ValueError(f"the contraction must be a multiple of {step}, not {k}")
     blocks = -(-k // size)
     s = _scales(s, "scale", (m, blocks), mx, dev)
-    lead = wq.shape[:-2]
     ws = _scales(ws, "weight scale", (*lead, n if mx else -(-n // 128), blocks), mx, dev)
-    if offsets is not None:
-        offsets = _offsets(offsets, dev)
-        if offsets.shape[0] != lead[0] + 1:
-            raise ValueError(f"offsets must be [{lead[0] + 1}], one more than there are weights")
-    y = _out(out, (m, n), out_dtype, dev)
-    return _launch(fn, q, s, wq, ws, y, n, k, offsets, wq.stride(0) if lead else 0, ws.stride(0) if lead else 0)
+    if offsets is None:
+        return _launch(fn, dev, q, s, wq, ws, _out(out, (m, n), out_dtype, q), n, k)
+    offsets = _offsets(offsets, dev)
+    if offsets.shape[0] != lead[0] + 1:
+        raise ValueError(f"offsets must be [{lead[0] + 1}], one more than there are weights")
+    return _launch(fn, dev, q, s, wq, ws, _out(out, (m, n), out_dtype, q), n, k, offsets, wq.stride(0), ws.stride(0))
 
 
 def blockfp8_matmul(q: torch.Tensor, S: torch.Tensor, wq: torch.Tensor, wS: torch.Tensor,
@@ -184,8 +188,8 @@ def mxfp8_matmul_wgrad(dyt: torch.Tensor, dys: torch.Tensor, xt: torch.Tensor, x
     if not isinstance(offsets, torch.Tensor):
         raise TypeError("offsets must be an int32 tensor")
     offsets = _offsets(offsets, dev)
-    y = _out(out, (offsets.shape[0] - 1, n, k), out_dtype, dev)
-    return _launch("mxq_matmul_wgrad", dyt, dys, xt, xs, y, k, tokens, offsets, y_stride=n * k)
+    y = _out(out, (offsets.shape[0] - 1, n, k), out_dtype, dyt)
+    return _launch("mxq_matmul_wgrad", dev, dyt, dys, xt, xs, y, k, tokens, offsets, y_stride=n * k)
 
 
 # ---------------------------------------------------------------------------
@@ -198,55 +202,63 @@ def _rows(t, what: str, shape, device=None) -> torch.Tensor:
         _mxq._need_bf16_cuda(t, what)
     else:
         _need(t, what, torch.bfloat16, device)
-    if t.dim() < 1:
-        raise ValueError(f"{what} must be [..., cols]")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must be {list(shape)}, not {list(t.shape)}")
-    if t.dim() != 2:
+        if t.shape != shape:
+            raise ValueError(f"{what} must be {list(shape)}, not {list(t.shape)}")
+    stride = t.stride()
+    if len(stride) != 2:
+        if not stride:
+            raise ValueError(f"{what} must be [..., cols]")
         t = t.reshape(t.shape[:-1].numel(), t.shape[-1])
-    ld, unit = t.stride()
-    if unit != 1 or ld % 8 or ld < t.shape[1] or t.data_ptr() % 16:
+        stride = t.stride()
+    if stride[1] != 1 or stride[0] & 7 or stride[0] < t.shape[1] or t.data_ptr() & 15:
         t = t.clone(memory_format=torch.contiguous_format)
     return t
 
 
 def _norm_weight(weight, cols: int, device) -> torch.Tensor:
-    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.bfloat16, torch.float32):
+    if not isinstance(weight, torch.Tensor) or (weight.dtype is not torch.bfloat16
+                                                and weight.dtype is not torch.float32):
         raise TypeError("weight must be a bfloat16 or float32 tensor")
     if weight.device != device:
         raise ValueError(f"weight must be on {device}")
-    if tuple(weight.shape) != (cols,):
+    if weight.shape != (cols,):
         raise ValueError(f"weight must be [{cols}]")
-    if not weight.is_contiguous() or weight.data_ptr() % 16:
+    if weight.stride(0) != 1 or weight.data_ptr() & 15:
         weight = weight.clone(memory_format=torch.contiguous_format)
     return weight
 
 
 def _rmsnorm(fn: str, mx: bool, x, weight, residual, eps, return_rstd, return_normed):
-    shape = x.shape if isinstance(x, torch.Tensor) else None
     x2 = _rows(x, "x", None)
-    dev = x2.device
+    dev, shape = x2.device, x.shape
     rows, cols = x2.shape
     step = 32 if mx else 8
     if cols % step:
         raise ValueError(f"x must have a multiple of {step} columns, not {cols}")
     weight = _norm_weight(weight, cols, dev)
-    r2 = h = rstd = y = None
+    q = x2.new_empty((rows, cols), dtype=torch.uint8)
+    if mx:
+        scale = x2.new_empty((rows, cols // 32), dtype=torch.uint8)
+    else:
+        scale = x2.new_empty((rows, -(-cols // 128)), dtype=torch.float32)
+    got = [q, scale]
+    rp = ldr = hp = sp = yp = 0
     if residual is not None:
-        r2 = _rows(residual, "residual", shape, dev)
-        h = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-    scale = torch.empty((rows, cols // 32 if mx else -(-cols // 128)),
-                        dtype=torch.uint8 if mx else torch.float32, device=dev)
+        residual = _rows(residual, "residual", shape, dev)
+        h = x2.new_empty(shape)
+        got.append(h)
+        rp, ldr, hp = residual.data_ptr(), residual.stride(0), h.data_ptr()
     if return_rstd:
-        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+        rstd = x2.new_empty((rows,), dtype=torch.float32)
+        got.append(rstd)
+        sp = rstd.data_ptr()
     if return_normed:
-        y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _call(fn, dev, _RMSNORM.pack(
-        x2.data_ptr(), 0 if r2 is None else r2.data_ptr(), weight.data_ptr(), q.data_ptr(), scale.data_ptr(),
-        0 if h is None else h.data_ptr(), 0 if y is None else y.data_ptr(), 0 if rstd is None else rstd.data_ptr(),
-        rows, cols, x2.stride(0), 0 if r2 is None else r2.stride(0), eps, weight.dtype is torch.float32, 0))
-    return tuple(t for t in (q, scale, h, rstd, y) if t is not None)
+        y = x2.new_empty(shape)
+        got.append(y)
+        yp = y.data_ptr()
+    _call(fn, dev, _RMSNORM.pack(x2.data_ptr(), rp, weight.data_ptr(), q.data_ptr(), scale.data_ptr(), hp, yp, sp,
+                                 rows, cols, x2.stride(0), ldr, eps, weight.dtype is torch.float32, 0))
+    return tuple(got)
 
 
 def rmsnorm_blockfp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
@@ -272,25 +284,27 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rs
     the norm returned it) and dh (the gradient that reaches h past the norm) bf16 [...,
     cols], rstd float32 [rows] as returned: (dx bf16 of dy's shape, the gradient of x
     and of the residual alike, dweight float32 [cols])."""
-    shape = dy.shape if isinstance(dy, torch.Tensor) else None
     dy2 = _rows(dy, "dy", None)
-    dev = dy2.device
+    dev, shape = dy2.device, dy.shape
     rows, cols = dy2.shape
     if cols % 8:
         raise ValueError(f"dy must have a multiple of 8 columns, not {cols}")
-    h2 = _rows(h, "h", shape, dev)
+    h = _rows(h, "h", shape, dev)
     weight = _norm_weight(weight, cols, dev)
     _need(rstd, "rstd", torch.float32, dev)
-    if tuple(rstd.shape) != (rows,):
+    if rstd.shape != (rows,):
         raise ValueError(f"rstd must be [{rows}]")
-    rstd = rstd.contiguous()
-    dh2 = None if dh is None else _rows(dh, "dh", shape, dev)
-    dx = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    dweight = torch.empty((cols,), dtype=torch.float32, device=dev)
+    if rows and rstd.stride(0) != 1:
+        rstd = rstd.contiguous()
+    gp = ldg = 0
+    if dh is not None:
+        dh = _rows(dh, "dh", shape, dev)
+        gp, ldg = dh.data_ptr(), dh.stride(0)
+    dx = dy2.new_empty(shape)
+    dweight = dy2.new_empty((cols,), dtype=torch.float32)
     nbytes = (_mxq._lib or _mxq.load()).mxq_rmsnorm_backward_workspace_size(rows, cols)
-    ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
+    ws = dy2.new_empty((nbytes,), dtype=torch.uint8)
     _call("mxq_rmsnorm_backward", dev, _RMSNORM_BACKWARD.pack(
-        dy2.data_ptr(), h2.data_ptr(), 0 if dh2 is None else dh2.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
-        dx.data_ptr(), dweight.data_ptr(), 0 if ws is None else ws.data_ptr(), nbytes, rows, cols, dy2.stride(0),
-        h2.stride(0), 0 if dh2 is None else dh2.stride(0), weight.dtype is torch.float32, 0))
+        dy2.data_ptr(), h.data_ptr(), gp, weight.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dweight.data_ptr(),
+        ws.data_ptr(), nbytes, rows, cols, dy2.stride(0), h.stride(0), ldg, weight.dtype is torch.float32, 0))
     return dx, dweight
