@@ -302,12 +302,15 @@ mxq_status fp8_matmul(bool mx, int ragged, const mxq_matmul_args *p, void *strea
     if (!p->y || (ragged != mxq::kDense && !p->offsets)) return MXQ_EINVAL;
     if (p->k > 0 && (!p->x || !p->w || !p->sx || !p->sw)) return MXQ_EINVAL;
     const int64_t blocks = (p->k + (mx ? 31 : 127)) / (mx ? 32 : 128);
-    if (p->ldx < p->k || p->ldw < p->k || p->ld_sx < blocks || p->ld_sw < blocks || p->ldy < p->n)
-        return MXQ_ESHAPE;
-    if (!aligned(p->x, 16) || !aligned(p->w, 16) || p->ldx % 16 || p->ldw % 16 ||
-        p->w_group_stride % 16 || !aligned(p->sx, mx ? 1 : 4) || !aligned(p->sw, mx ? 1 : 4) ||
-        !aligned(p->y, p->out_fp32 ? 4 : 2) || !aligned(p->offsets, 4))
-        return MXQ_EALIGN;
+    if (p->ldy < p->n) return MXQ_ESHAPE;
+    if (!aligned(p->y, p->out_fp32 ? 4 : 2) || !aligned(p->offsets, 4)) return MXQ_EALIGN;
+    if (p->k > 0) {  // else nothing of the operands is read
+        if (p->ldx < p->k || p->ldw < p->k || p->ld_sx < blocks || p->ld_sw < blocks)
+            return MXQ_ESHAPE;
+        if (!aligned(p->x, 16) || !aligned(p->w, 16) || p->ldx % 16 || p->ldw % 16 ||
+            p->w_group_stride % 16 || !aligned(p->sx, mx ? 1 : 4) || !aligned(p->sw, mx ? 1 : 4))
+            return MXQ_EALIGN;
+    }
     // rows of a tile are reached with 32-bit offsets, everything else with 64
     constexpr int64_t most = 0x7FFFFF00, most_ld = (int64_t)1 << 22;
     if (p->m > most || p->n > most || p->ldx > most_ld || p->ldw > most_ld ||

@@ -337,9 +337,11 @@ hipError_t launch_rmsnorm_back(const RmsNormBack &a, hipStream_t stream)
         default: go(std::integral_constant<int, 8>{}, F); break;
         }
     };
-    a.weight_f32 ? by_waves(std::true_type{}) : by_waves(std::false_type{});
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (parts > 0) {  // no rows: only dweight's zeros
+        a.weight_f32 ? by_waves(std::true_type{}) : by_waves(std::false_type{});
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     rmsnorm_dweight_kernel<<<dim3((unsigned)((a.cols + 63) / 64)), dim3(1024), 0, stream>>>(a.part, parts, a.cols,
                                                                                          a.dweight);
     return hipGetLastError();
