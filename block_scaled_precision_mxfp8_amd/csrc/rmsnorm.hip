@@ -93,7 +93,7 @@ __device__ __forceinline__ uint32_t signs_of(const float *f)
 
 // kWaves waves on a row; a workgroup has at least four.
 template <bool kMX, int kWaves, bool kWeightF32>
-__global__ __launch_bounds__(kWaves < 4 ? 256 : kWaves * 64) void rmsnorm_kernel(RmsNorm a)
+__global__ __launch_bounds__(kWaves < 4 ? 256 : kWaves * 64, 8) void rmsnorm_kernel(RmsNorm a)
 {
     constexpr int kThreads = kWaves < 4 ? 256 : kWaves * 64, kRows = kThreads / (kWaves * 64);
     __shared__ double red[1][8];
@@ -153,7 +153,24 @@ __global__ __launch_bounds__(kWaves < 4 ? 256 : kWaves * 64) void rmsnorm_kernel
         uint2 c;
         if constexpr (kMX) {
             m = quad_max(m);
-            const uint32_t e = m >> 23, s = e >= 0xFFu ? 0xFFu : e > 8u ? e - 8u : 0u;
+            // A largest value just below a power of two may have been rounded up to it:
+            // then its group keeps the lower scale.
+            uint32_t below = 0;
+            if (wave_any((m & 0x7FFFFFu) == 0 && m != 0 && m < 0x7F800000u)) {
+                uint32_t reached = 0;  // some value is that power or more
+#pragma unroll 1  // seldom, and in few registers: again from the start, a value at a time
+                for (int j = 0; j < 8 && in; ++j) {
+                    const uint32_t pair = j < 2 ? v[i].x : j < 4 ? v[i].y : j < 6 ? v[i].z : v[i].w;
+                    const float x = j & 1 ? bf16hi_to_f32(pair) : bf16lo_to_f32(pair);
+                    const float wj = kWeightF32 ? static_cast<const float *>(a.weight)[col + j]
+                                                : bf16lo_to_f32(static_cast<const uint16_t *>(a.weight)[col + j]);
+                    const float t = r * wj, low = __builtin_fmaf(r, wj, -t) + r_low * wj;
+                    const float yj = __builtin_fmaf(x, t, x * low), rest = __builtin_fmaf(x, t, -yj) + x * low;
+                    if ((__float_as_uint(yj) & 0x7FFFFFFFu) == m && (yj > 0 ? rest >= 0 : rest <= 0)) reached = 1;
+                }
+                below = (m & 0x7FFFFFu) == 0 && m != 0 && m < 0x7F800000u && quad_max(reached) == 0;
+            }
+            const uint32_t e = (m >> 23) - below, s = e >= 0xFFu ? 0xFFu : e > 8u ? e - 8u : 0u;
             Row8 t;
 #pragma unroll
             for (int j = 0; j < 8; ++j) t.f[j] = __builtin_amdgcn_ldexpf(y.f[j], 127 - (int)s);
