@@ -77,11 +77,11 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
     // -- what this wave brings to LDS: kLoads times 8 rows of x or of w
     const bool of_x = wave * kLoads * 8 < BM;
     const int first = of_x ? wave * kLoads * 8 : wave * kLoads * 8 - BM;
-    const int64_t ld = of_x ? a.ldx : a.ldw;
+    const int64_t ld = __builtin_amdgcn_readfirstlane((int)(of_x ? a.ldx : a.ldw));
     const uint8_t *base = of_x ? a.x + (int64_t)row0 * a.ldx
                                : a.w + (kRagged == kRows ? group * a.w_stride : 0) +
                                      (int64_t)col0 * a.ldw;
-    const int last = (of_x ? row_end - row0 : col_end - col0) - 1;  // rows past it repeat it: their results are dropped
+    const int last = __builtin_amdgcn_readfirstlane((of_x ? row_end - row0 : col_end - col0) - 1);  // rows past it repeat it: their results are dropped
     // Row r's 16-byte piece c lies at piece c ^ (r / 2 % 8) of its line in LDS: sixteen
     // rows' pieces of one c, read together, then fall on all 64 banks.  (c ^ (r % 8), for
     // 32 banks, leaves two on each: block-FP8 8192 x 8192 x 7168 took 5 % longer.)
@@ -97,7 +97,8 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
         piece_at[1] = (chunk ^ 4) * 16 | ((int)((chunk ^ 4) * 16) > left ? kNowhere : 0u);
     };
     auto fill_one = [&](int32_t s, int i) {
-        const int r = first + i * 8;
+        int r = first + i * 8;
+        asm volatile("" : "+s"(r));  // a few scalar operations here take no register for good
         const uint32_t in_rows = min(vrow, (uint32_t)__builtin_amdgcn_readfirstlane(max(min(last - r, 7), 0) * (int)ld));
         load_to_lds(rsrc, lds0 + (s & 1) * kStage + (wave * kLoads + i) * 1024, in_rows + piece_at[i & 1],
                     __builtin_amdgcn_readfirstlane(min(r, last) * (int)ld + k0 + s * kStep));
@@ -166,14 +167,13 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
     // where step s finds them
     auto scales_of = [&](int32_t s) { return scales[s / 4 == last_group ? 2 : s / 4 & 1][s & 3]; };
 
-    // -- operands: four places of a row's line, by the half of the step and of the operand
-    uint32_t at[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) at[i] = p * kStep + (((2 * i + h) ^ (p >> 1 & 7)) << 4);
-    auto operand = [&](uint32_t stage, int row, int t) {  // rows row .., half t
-        const uint8_t *q = lds + stage + row * kStep;
-        return join(*reinterpret_cast<const uint4 *>(q + at[2 * t]),
-                    *reinterpret_cast<const uint4 *>(q + at[2 * t + 1]));
+    // -- operands: lane (p, h) finds piece 2 i + h of row p's line at place ^ 32 i
+    uint32_t place = p * kStep + ((h ^ (p >> 1 & 7)) << 4);
+    auto piece = [&](uint32_t stage, int row, int i) {  // 16 bytes of rows row ..
+        return *reinterpret_cast<const uint4 *>(lds + ((place + stage) ^ (32 * i)) + row * kStep);
+    };
+    auto operand = [&](uint32_t stage, int row, int t) {  // half t of the step
+        return join(piece(stage, row, 2 * t), piece(stage, row, 2 * t + 1));
     };
 
     f32x16 acc[RT][CT];
@@ -227,9 +227,6 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
         for (int32_t s = 0; s < steps; ++s) {
             const uint32_t stage = (s & 1) * kStage;
             const uint32_t *sc = scales_of(s);
-            auto piece = [&](int row, int i) {  // 16 bytes of the wave's rows row ..
-                return *reinterpret_cast<const uint4 *>(lds + stage + row * kStep + at[i]);
-            };
             if constexpr (kMX) {
                 uint32_t sx[CT], sr[RT];
 #pragma unroll
@@ -241,11 +238,11 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
                     bf16x8 b[CT][2];
 #pragma unroll
                     for (int c = 0; c < CT; ++c)
-                        decode16(b[c], piece((wt * CT + c) * 32, i), e8m0_to_f32((sx[c] >> (8 * i)) & 0xFF));
+                        decode16(b[c], piece(stage, (wt * CT + c) * 32, i), e8m0_to_f32((sx[c] >> (8 * i)) & 0xFF));
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
                         bf16x8 w[2];
-                        decode16(w, piece(BM + (wn * RT + r) * 32, i), e8m0_to_f32((sr[r] >> (8 * i)) & 0xFF));
+                        decode16(w, piece(stage, BM + (wn * RT + r) * 32, i), e8m0_to_f32((sr[r] >> (8 * i)) & 0xFF));
 #pragma unroll
                         for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -258,7 +255,7 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
 #pragma unroll
                 for (int c = 0; c < CT; ++c)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) decode16(b[c][i], piece((wt * CT + c) * 32, i), 1.0f);
+                    for (int i = 0; i < 4; ++i) decode16(b[c][i], piece(stage, (wt * CT + c) * 32, i), 1.0f);
                 const float swv = __uint_as_float(sc[BM + wn]);
                 float f[CT];
 #pragma unroll
@@ -267,7 +264,7 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
                 for (int r = 0; r < RT; ++r) {
                     bf16x8 w[4][2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) decode16(w[i], piece(BM + (wn * RT + r) * 32, i), 1.0f);
+                    for (int i = 0; i < 4; ++i) decode16(w[i], piece(stage, BM + (wn * RT + r) * 32, i), 1.0f);
 #pragma unroll
                     for (int c = 0; c < CT; ++c) {
                         f32x16 q{};
@@ -337,38 +334,50 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
             }
         }
     } else {
-        for (int32_t s = 0; s < steps; ++s) {
-            const uint32_t stage = (s & 1) * kStage;
+        // A step's last weight rows are multiplied behind its barrier, under the next
+        // step's tokens coming to registers.
+        i32x8 b0[CT][2], b1[CT][2];
+        auto fetch_b = [&](i32x8(&b)[CT][2], int32_t s) {
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) b[c][t] = operand((s & 1) * kStage, (wt * CT + c) * 32, t);
+        };
+        auto step = [&](const i32x8(&b)[CT][2], i32x8(&next)[CT][2], int32_t s) {
+            asm volatile("" : "+v"(place));  // its sums anew each step: few registers are left
             const uint32_t *sc = scales_of(s);
             const float swv = __uint_as_float(sc[BM + wn]);
             float f[CT];
 #pragma unroll
             for (int c = 0; c < CT; ++c) f[c] = __uint_as_float(sc[(wt * CT + c) * 32 + p]) * swv;
-            i32x8 b[CT][2];
-#pragma unroll
-            for (int c = 0; c < CT; ++c)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) b[c][t] = operand(stage, (wt * CT + c) * 32, t);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const i32x8 w0 = operand(stage, BM + (wn * RT + r) * 32, 0);
-                const i32x8 w1 = operand(stage, BM + (wn * RT + r) * 32, 1);
+                const i32x8 w0 = operand((s & 1) * kStage, BM + (wn * RT + r) * 32, 0);
+                const i32x8 w1 = operand((s & 1) * kStage, BM + (wn * RT + r) * 32, 1);
+                if (r == RT - 1) {
+                    turn(s);
+                    fetch_b(next, s + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
 #pragma unroll
                 for (int c = 0; c < CT; ++c) {
                     f32x16 q{};
                     q = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w0, b[c][0], q, 0, 0, 0, 0, 0, 0);
                     q = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w1, b[c][1], q, 0, 0, 0, 0, 0, 0);
+                    if (r == RT - 1) {
+#pragma unroll
+                        for (int i = 0; i < kLoads / CT; ++i) fill_one(s + 2, c * (kLoads / CT) + i);
+                    }
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         acc[r][c][i] = __builtin_fmaf(q[i], f[c], acc[r][c][i]);
                 }
-                if (r == 0) aim(s + 1);
-                if (s > 0) {
-#pragma unroll
-                    for (int i = 0; i < kLoads / RT; ++i) fill_one(s + 1, r * (kLoads / RT) + i);
-                }
             }
-            turn(s);
+        };
+        if (steps > 0) fetch_b(b0, 0);
+        for (int32_t s = 0; s < steps; s += 2) {
+            step(b0, b1, s);
+            if (s + 1 < steps) step(b1, b0, s + 1);
         }
     }
 
@@ -431,8 +440,12 @@ hipError_t launch(const Fp8Matmul &a, hipStream_t stream)
     TileGrid g;
     g.tm = (a.m + BM - 1) / BM + (kRagged == kRows ? a.groups : 0);
     g.tn = (a.n + BN - 1) / BN;
-    g.sm = g.tm < 8 ? g.tm : 8;
-    g.sn = 32 / g.sm < g.tn ? 32 / g.sm : g.tn;
+    auto parts = [](int32_t n, int32_t most) {  // n cut evenly into parts of at most `most`
+        const int32_t cuts = (n + most - 1) / most;
+        return (n + cuts - 1) / cuts;
+    };
+    g.sm = parts(g.tm, 8);
+    g.sn = parts(g.tn, 32 / g.sm);
     if (kRagged == kContraction)  // every group's blocks are dealt to eight XCDs anew: smaller ones come out even
         while (g.sm * g.sn > 8) (g.sm > g.sn ? g.sm : g.sn) /= 2;
     g.bm = (g.tm + g.sm - 1) / g.sm;
