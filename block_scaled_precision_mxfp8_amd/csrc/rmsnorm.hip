@@ -93,7 +93,7 @@ __device__ __forceinline__ uint32_t signs_of(const float *f)
 
 // kWaves waves on a row; a workgroup has at least four.
 template <bool kMX, int kWaves, bool kWeightF32>
-__global__ __launch_bounds__(kWaves < 4 ? 256 : kWaves * 64, 8) void rmsnorm_kernel(RmsNorm a)
+__global__ __launch_bounds__(kWaves < 4 ? 256 : kWaves * 64, 7) void rmsnorm_kernel(RmsNorm a)
 {
     constexpr int kThreads = kWaves < 4 ? 256 : kWaves * 64, kRows = kThreads / (kWaves * 64);
     __shared__ double red[1][8];
@@ -153,27 +153,43 @@ __global__ __launch_bounds__(kWaves < 4 ? 256 : kWaves * 64, 8) void rmsnorm_ker
         uint2 c;
         if constexpr (kMX) {
             m = quad_max(m);
-            // A largest value just below a power of two may have been rounded up to it:
-            // then its group keeps the lower scale.
+            // What y lost when it was rounded to 32 bits counts where y has come to lie
+            // on a border: then it is worked out again, seldom and in few registers.
+            auto rest = [&](int j) {  // above 0: the magnitude of value j is larger than y has it
+                const uint32_t pair = j < 2 ? v[i].x : j < 4 ? v[i].y : j < 6 ? v[i].z : v[i].w;
+                const float x = j & 1 ? bf16hi_to_f32(pair) : bf16lo_to_f32(pair);
+                const float wj = kWeightF32 ? static_cast<const float *>(a.weight)[col + j]
+                                            : bf16lo_to_f32(static_cast<const uint16_t *>(a.weight)[col + j]);
+                const float t = r * wj, low = __builtin_fmaf(r, wj, -t) + r_low * wj;
+                const float yj = __builtin_fmaf(x, t, x * low);
+                return (__builtin_fmaf(x, t, -yj) + x * low) * __builtin_copysignf(1.0f, yj);
+            };
+            // a largest value just below a power of two, rounded up to it, keeps the lower scale
             uint32_t below = 0;
-            if (wave_any((m & 0x7FFFFFu) == 0 && m != 0 && m < 0x7F800000u)) {
+            const bool power = (m & 0x7FFFFFu) == 0 && m != 0 && m < 0x7F800000u;
+            if (wave_any(power)) {
                 uint32_t reached = 0;  // some value is that power or more
-#pragma unroll 1  // seldom, and in few registers: again from the start, a value at a time
-                for (int j = 0; j < 8 && in; ++j) {
-                    const uint32_t pair = j < 2 ? v[i].x : j < 4 ? v[i].y : j < 6 ? v[i].z : v[i].w;
-                    const float x = j & 1 ? bf16hi_to_f32(pair) : bf16lo_to_f32(pair);
-                    const float wj = kWeightF32 ? static_cast<const float *>(a.weight)[col + j]
-                                                : bf16lo_to_f32(static_cast<const uint16_t *>(a.weight)[col + j]);
-                    const float t = r * wj, low = __builtin_fmaf(r, wj, -t) + r_low * wj;
-                    const float yj = __builtin_fmaf(x, t, x * low), rest = __builtin_fmaf(x, t, -yj) + x * low;
-                    if ((__float_as_uint(yj) & 0x7FFFFFFFu) == m && (yj > 0 ? rest >= 0 : rest <= 0)) reached = 1;
-                }
-                below = (m & 0x7FFFFFu) == 0 && m != 0 && m < 0x7F800000u && quad_max(reached) == 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (in && (__float_as_uint(y.f[j]) & 0x7FFFFFFFu) == m && rest(j) >= 0.f) reached = 1;
+                below = power && quad_max(reached) == 0;
             }
             const uint32_t e = (m >> 23) - below, s = e >= 0xFFu ? 0xFFu : e > 8u ? e - 8u : 0u;
             Row8 t;
 #pragma unroll
             for (int j = 0; j < 8; ++j) t.f[j] = __builtin_amdgcn_ldexpf(y.f[j], 127 - (int)s);
+            // halfway between two codes, as rounded: to the side where it was
+            uint32_t halfway = ~0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) halfway = min(halfway, (__float_as_uint(t.f[j]) << 12) + 0x80000000u);
+            if (wave_any(halfway == 0)) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (in && s != 0xFFu && __float_as_uint(t.f[j]) << 12 == 0x80000000u) {
+                        const float o = rest(j);
+                        t.f[j] = __uint_as_float(__float_as_uint(t.f[j]) + (o > 0.f ? 1u : o < 0.f ? ~0u : 0u));
+                    }
+            }
             c.x = cvt_fp8x2_f32<true>(cvt_fp8x2_f32<false>(0u, t.f[0], t.f[1]), t.f[2], t.f[3]);
             c.y = cvt_fp8x2_f32<true>(cvt_fp8x2_f32<false>(0u, t.f[4], t.f[5]), t.f[6], t.f[7]);
             if (s == 0xFFu) c = make_uint2(0x7F7F7F7Fu | signs_of(y.f), 0x7F7F7F7Fu | signs_of(y.f + 4));
