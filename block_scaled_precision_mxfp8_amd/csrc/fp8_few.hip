@@ -203,7 +203,7 @@ hipError_t launch(const Fp8Matmul &a, hipStream_t stream)
 {
     const int64_t ct = (a.n + R * 16 - 1) / (R * 16);
     const int64_t rt = (a.m + T * 16 - 1) / (T * 16) + (kRagged == kRows ? a.groups : 0);
-    if (ct > 0x7FFFFFFF || rt > 65535) return hipErrorInvalidConfiguration;
+    if (ct * (W * 64) > 0xFFFFFFFF || rt > 65535) return hipErrorInvalidConfiguration;  // a grid's threads fit 32 bits
     const dim3 grid((unsigned)ct, (unsigned)rt), block(W * 64);
     if (a.out_f32) few_kernel<kMX, true, kRagged, R, T, W, D><<<grid, block, 0, stream>>>(a);
     else few_kernel<kMX, false, kRagged, R, T, W, D><<<grid, block, 0, stream>>>(a);

@@ -452,7 +452,7 @@ hipError_t launch(const Fp8Matmul &a, hipStream_t stream)
     g.bn = (g.tn + g.sn - 1) / g.sn;
     g.groups = kRagged == kContraction ? a.groups : 1;
     const int64_t wgs = ((int64_t)g.bm * g.bn + 7) / 8 * 8 * g.sm * g.sn * g.groups;
-    if (wgs > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    if (wgs * (WT * WN * 64) > 0xFFFFFFFF) return hipErrorInvalidConfiguration;  // a grid's threads fit 32 bits
     tile_kernel<kMX, kExact, kRagged, WT, WN, CT, RT>
         <<<dim3((unsigned)wgs), dim3(WT * WN * 64), 0, stream>>>(a, g);
     return hipGetLastError();
@@ -477,7 +477,7 @@ hipError_t launch_fp8_matmul(bool mx, int ragged, const Fp8Matmul &a, hipStream_
     // and smaller workgroups are ahead although they read the weights again for every 64.
     if (ragged == kDense && (a.m <= 64 || (int64_t)((a.m + 63) / 64) * a.n <= 16384))
         return launch_fp8_few(mx, ragged, a.m, a, stream);
-    if (ragged == kRows && a.m <= (int64_t)32 * a.groups && a.m / 32 + a.groups <= 65535)
+    if (ragged == kRows && a.m <= (int64_t)32 * a.groups && a.m / 32 + a.groups < 65535)
         return launch_fp8_few(mx, ragged, (a.m - 1) / a.groups + 1, a, stream);
     if (mx)
         return ragged == kDense ? pick<true, kDense>(a, stream)

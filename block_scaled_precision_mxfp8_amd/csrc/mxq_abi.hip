@@ -284,8 +284,7 @@ mxq_status rmsnorm(bool mx, const mxq_rmsnorm_args *p, void *stream)
     a.ldr = p->ld_residual;
     a.eps = p->eps;
     a.weight_f32 = p->weight_fp32 != 0;
-    const hipError_t e = mxq::launch_rmsnorm(mx, a, as_stream(stream));
-    return e == hipErrorInvalidConfiguration ? MXQ_ESIZE : from_hip(e);
+    return from_hip(mxq::launch_rmsnorm(mx, a, as_stream(stream)));
 }
 
 // What the five products with 8-bit operands share; `ragged` is what offsets cut.

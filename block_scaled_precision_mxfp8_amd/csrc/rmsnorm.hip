@@ -337,10 +337,22 @@ int32_t rmsnorm_back_parts(int64_t rows, int64_t cols)
 hipError_t launch_rmsnorm(bool mx, const RmsNorm &a, hipStream_t stream)
 {
     const int w = waves_for(a.cols), per = w < 4 ? 4 / w : 1;
-    const int64_t grid = (a.rows + per - 1) / per;
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
     auto go = [&](auto MX, auto W, auto F) {
-        rmsnorm_kernel<MX, W, F><<<dim3((unsigned)grid), dim3(W < 4 ? 256 : W * 64), 0, stream>>>(a);
+        constexpr int kThreads = W < 4 ? 256 : W * 64;
+        const int64_t most = ((int64_t)1 << 31) / kThreads * per;  // rows of one launch, whose threads 32 bits count
+        for (int64_t first = 0; first < a.rows; first += most) {
+            RmsNorm b = a;
+            b.rows = a.rows - first < most ? a.rows - first : most;
+            b.x += first * a.ldx;
+            if (a.residual) b.residual += first * a.ldr;
+            b.q += first * a.cols;
+            if (MX) b.scale = static_cast<uint8_t *>(a.scale) + first * (a.cols / 32);
+            else b.scale = static_cast<float *>(a.scale) + first * ((a.cols + 127) / 128);
+            if (a.h) b.h += first * a.cols;
+            if (a.y) b.y += first * a.cols;
+            if (a.rstd) b.rstd += first;
+            rmsnorm_kernel<MX, W, F><<<dim3((unsigned)((b.rows + per - 1) / per)), dim3(kThreads), 0, stream>>>(b);
+        }
     };
     auto by_waves = [&](auto MX, auto F) {
         switch (w) {

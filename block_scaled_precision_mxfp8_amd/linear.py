@@ -252,6 +252,8 @@ def _rmsnorm(fn: str, mx: bool, x, weight, residual, eps, return_rstd, return_no
         rstd = x2.new_empty((rows,), dtype=torch.float32)
         got.append(rstd)
         sp = rstd.data_ptr()
+        if not cols:
+            rstd.fill_(float("nan"))  # the mean of nothing
     if return_normed:
         y = x2.new_empty(shape)
         got.append(y)

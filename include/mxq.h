@@ -505,8 +505,9 @@ mxq_status nvfp4_matvec(const uint16_t *x, int64_t tokens, int64_t ldx, const ui
  *   y       optional [rows, cols] bf16: y rounded (for a column-wise quantizer)
  *   rstd    optional fp32 [rows]: r
  * x, residual, weight, h and y are 16-byte aligned.  Shape: cols a multiple of 8
- * (blockfp8) or 32, at most 16384 (MXQ_ESIZE).  The sum of squares is fp32: values
- * over 2^63 / sqrt(cols) make it infinite, and y zero.
+ * (blockfp8) or 32, at most 16384 (MXQ_ESIZE).  Squares are summed in fp32, eight at a
+ * time, then in fp64: values of 2^62 make the sum infinite, and y zero.  cols == 0
+ * writes nothing, rstd neither.
  */
 typedef struct mxq_rmsnorm_args {
     const uint16_t *x, *residual;
@@ -587,7 +588,9 @@ mxq_status mxq_rmsnorm_backward(const mxq_rmsnorm_backward_args *args, void *str
  *       transposed gradient [out, tokens] and w = the transposed input [in,
  *       tokens], both from mxq_quantize_colwise_t, y is a linear layer's weight
  *       gradient [groups, out, in].
- * At most 65535 groups; offsets and groups are NULL and 0 for the dense forms.
+ * At most 65535 groups, and what one launch holds: below 2^28 columns for a few tokens,
+ * below 2^39 results for many (MXQ_ESIZE otherwise); offsets and groups are NULL
+ * and 0 for the dense forms.
  * NaN codes and scales reach the sums they belong to.  The order of summation
  * depends on shapes alone; sums of MXFP8 are kept in the matrix cores, whose
  * fp32 additions cut off what they cannot hold (block-FP8: within 128 k).

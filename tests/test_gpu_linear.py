@@ -407,3 +407,16 @@ def test_streams_and_graphs(gpu):
         torch.cuda.synchronize()
         for a, b in zip(held, eager):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("groups", [65534, 65535])
+@pytest.mark.parametrize("m", [1, 40])
+def test_grouped_most_groups(gpu, groups, m):
+    g = ref.generator(groups + m)
+    q, s, w, ws = ref.block_operands(g, m, 8, 16, (groups,))
+    of = torch.randint(0, groups, (m,), generator=g, device="cuda").sort().values
+    of[-1] = groups - 1
+    off = torch.searchsorted(of, torch.arange(groups + 1, device="cuda")).int()
+    y = gpu.blockfp8_matmul_grouped(q, s, w, ws, off, out_dtype=F32)
+    for i in range(m):
+        ref.check(y[i:i + 1], ref.x_block(q[i:i + 1], s[i:i + 1]), ref.w_block(w[of[i]], ws[of[i]]))

@@ -239,3 +239,59 @@ def test_offsets_past_32_bits(gpu):
     ex, ew = ref.norm_backward(x[-3:], x[-3:], w, r[-3:], None)
     assert ((dx[-3:].double() - ex).abs() <= 2.0 ** -7 * ex.abs() + 1e-5).all()
     assert ((dw.double() - ew).abs() <= 1e-4 * ew.abs() + 1e-4).all()
+
+
+def test_more_rows_than_one_launch_has(gpu):
+    """Rows of one wave, four to a workgroup of 256 threads: 2^31 threads are 2^25 rows."""
+    rows = (1 << 25) + 9
+    g = ref.generator(12)
+    x = torch.ones(rows, 8, dtype=BF16, device="cuda")
+    at = torch.tensor([0, 1, (1 << 25) - 1, 1 << 25, (1 << 25) + 1, rows - 1], device="cuda")
+    x[at] = torch.randn(6, 8, generator=g, device="cuda").bfloat16()
+    w = torch.rand(8, generator=g, device="cuda").bfloat16()
+    q, s, h, r, y16 = gpu.rmsnorm_blockfp8(x, w, x, return_rstd=True, return_normed=True)
+    assert torch.equal(h, x + x)
+    _, er, ey = ref.norm(x[at], x[at], w, 1e-6)
+    check_codes("block", q[at], s[at], ey)
+    assert ((r[at].double() - er).abs() <= 2.0 ** -22 * er).all()
+    assert ((y16[at].double() - ey).abs() <= (2.0 ** -8 + 2.0 ** -20) * ey.abs()).all()
+    rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert (r[rest] == r[2]).all() and (s[rest] == s[2]).all() and (q[rest] == q[2]).all()
+
+
+def test_no_columns(gpu):
+    x = torch.zeros(3, 0, dtype=BF16, device="cuda")
+    w = torch.zeros(0, device="cuda")
+    for call in (gpu.rmsnorm_blockfp8, gpu.rmsnorm_mxfp8):
+        q, s, r = call(x, w, return_rstd=True)
+        assert q.shape == s.shape == (3, 0) and torch.isnan(r).all()
+    dx, dw = gpu.rmsnorm_backward(x, x, w, r)
+    assert dx.shape == (3, 0) and dw.shape == (0,)
+
+
+@pytest.mark.parametrize("cols", [96, 5120])
+def test_outputs_in_place(gpu, cols):
+    """h over x or the residual, dx over dy, dh or h: as into memory of their own."""
+    from block_scaled_precision_mxfp8_amd import linear
+    g = ref.generator(13)
+    x, res, dh = (torch.randn(30, cols, generator=g, device="cuda").bfloat16() for _ in range(3))
+    w = torch.rand(cols, generator=g, device="cuda")
+    q, s, h, r = gpu.rmsnorm_mxfp8(x, w, res, return_rstd=True)
+    for over in (0, 1):
+        a = [x.clone(), res.clone()]
+        q2, s2 = torch.empty_like(q), torch.empty_like(s)
+        linear._call("mxq_rmsnorm", x.device, linear._RMSNORM.pack(
+            a[0].data_ptr(), a[1].data_ptr(), w.data_ptr(), q2.data_ptr(), s2.data_ptr(), a[over].data_ptr(), 0, 0,
+            30, cols, cols, cols, 1e-6, 1, 0))
+        assert torch.equal(q, q2) and torch.equal(s, s2) and torch.equal(h, a[over])
+    dx, dw = gpu.rmsnorm_backward(x, h, w, r, dh=dh)
+    for over in range(3):
+        a = [x.clone(), h.clone(), dh.clone()]
+        dw2 = torch.empty_like(dw)
+        n = gpu.load().mxq_rmsnorm_backward_workspace_size(30, cols)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        linear._call("mxq_rmsnorm_backward", x.device, linear._RMSNORM_BACKWARD.pack(
+            *(t.data_ptr() for t in a), w.data_ptr(), r.data_ptr(), a[over].data_ptr(), dw2.data_ptr(),
+            ws.data_ptr(), n, 30, cols, cols, cols, cols, 1, 0))
+        assert torch.equal(dx, a[over]) and torch.equal(dw, dw2)
