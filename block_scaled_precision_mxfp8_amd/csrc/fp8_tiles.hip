@@ -15,6 +15,21 @@
 //   Block-FP8: 128 k are multiplied unscaled, from zero, and leave with one FMA an
 //   element: acc += p * (sx * sw).  A lane has one token and a wave's weight rows lie in
 //   one tile of 128, so the factor is one number per lane and 32 tokens.
+//
+// The 8-bit instruction keeps, of 8 neighbouring k, what lies above 2^-13 of their
+// largest product (measured): 5e-5 of a sum's norm, a thirtieth of what rounding to bf16
+// takes.  Results in fp32 (kExact) are for more than that, so there the codes are made
+// bf16, without loss, and v_mfma_f32_32x32x16_bf16 multiplies: 1.5e-7, at half the rate.
+//
+// Bound, where the contraction is long, by the matrix cores: 4096 x 8192 x 8192 MXFP8
+// 234 us (2.35 PFLOP/s; the matrix cores busy 80 % of it at 2.1 GHz), 8192 x 7168 x 7168
+// block-FP8 428 us (1.97 PFLOP/s; 3.5 rounds of tiles cost as much as 4, and the FMAs
+// with the scales run beside the products only in part).  So LDS is filled straight from
+// memory, two steps deep, and what a step has to read from it is read under the last
+// step's products.  Where it is short, by what does not overlap in a CU that holds one
+// tile: 16384 tokens of 32 groups as the contraction of 2048 x 7168 weight gradients,
+// four steps a tile, take 485 us, of which the stores alone are 181, the steps 240
+// and the start of 7168 workgroups 106.
 
 #include "fp8_matmul.hpp"
 #include "launch.hpp"
@@ -81,7 +96,8 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
     const uint8_t *base = of_x ? a.x + (int64_t)row0 * a.ldx
                                : a.w + (kRagged == kRows ? group * a.w_stride : 0) +
                                      (int64_t)col0 * a.ldw;
-    const int last = __builtin_amdgcn_readfirstlane((of_x ? row_end - row0 : col_end - col0) - 1);  // rows past it repeat it: their results are dropped
+    // rows past the last repeat it: their results are dropped
+    const int last = __builtin_amdgcn_readfirstlane((of_x ? row_end - row0 : col_end - col0) - 1);
     // Row r's 16-byte piece c lies at piece c ^ (r / 2 % 8) of its line in LDS: sixteen
     // rows' pieces of one c, read together, then fall on all 64 banks.  (c ^ (r % 8), for
     // 32 banks, leaves two on each: block-FP8 8192 x 8192 x 7168 took 5 % longer.)
@@ -381,9 +397,10 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
         }
     }
 
-    // -- out (what is still on its way to LDS, nothing but zeros, is let in first): a wave turns 32 tokens at a time around in 8 KiB of LDS and writes rows of
-    // 256 bytes, 16 a lane: bf16 for a wave's 128 columns (64 in the small tiles), fp32
-    // for 64.  Piece j of row r, two lanes' worth, lies at j ^ (r % 8).
+    // -- out (what is still on its way to LDS, nothing but zeros, is let in first): a
+    // wave turns 32 tokens at a time around in LDS and writes whole rows of its columns,
+    // 16 bytes a lane: 256 bytes of bf16 (128 in the small tiles) or fp32.  Piece j of row
+    // r lies at j ^ (r % 8).
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     constexpr int kCols = RT * 32, kSize = kExact ? 4 : 2, kRow = kCols * kSize;
@@ -416,8 +433,8 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
             for (int i = 0; i < 32 / kRowsAt; ++i) {
                 const int tr = i * kRowsAt + lane / kPieces, j = lane % kPieces;
                 const uint4 v = *reinterpret_cast<const uint4 *>(mine + tr * kRow + ((j ^ (tr & 7)) << 4));
-                if (tr < rows)
-                    *reinterpret_cast<uint4 *>(y + ((int64_t)(trow + tr) * a.ldy + wcol) * kSize + j * 16) = v;
+                if (tr < rows)  // past the caches, which keep the operands: 2 to 4 % less time
+                    st16<true>(y + ((int64_t)(trow + tr) * a.ldy + wcol) * kSize + j * 16, v);
             }
         } else if (cols > 0) {
             for (int tr = 0; tr < rows; ++tr)
@@ -462,8 +479,9 @@ template <bool kMX, int kRagged>
 hipError_t pick(const Fp8Matmul &a, hipStream_t stream)
 {
     if (a.out_f32) return launch<kMX, true, kRagged, 2, 2, 2, 2>(a, stream);
-    // 256 x 256 tiles, one to a CU, or 128 x 128, two: 1.8 us a step for 256 of the ones
-    // (k = 7168, 101 us), 0.85 for up to 256 of the others, 1.3 for 512 (64 us)
+    // 256 x 256 tiles, one to a CU, or 128 x 128, two.  A round of 256 large ones takes
+    // 1.8 us a step (k = 7168: 101 us), as many small ones 0.85, 512 of them 1.3 (73 us): so
+    // much work is four rounds of these, or three quarters of a round of the large.
     const int64_t big = (int64_t)((a.m + 255) / 256) * ((a.n + 255) / 256) * (kRagged == kContraction ? a.groups : 1);
     if (big >= 192) return launch<kMX, false, kRagged, 4, 2, 2, 4>(a, stream);
     return launch<kMX, false, kRagged, 2, 2, 2, 2>(a, stream);
