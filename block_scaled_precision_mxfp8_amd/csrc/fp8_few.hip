@@ -13,6 +13,10 @@
 // the bytes k = 16 g .. and 64 + 16 g .., the scale of its group 32 g .., and of the
 // result column p in rows 4 g + 0..3.  fp32 results go through
 // v_mfma_f32_16x16x32_bf16, eight bytes of a lane at a time.
+//
+// Bound by the weights' bytes where there are many: 512 rows of 128 groups of 2048 x 7168
+// 246 to 258 us, 7.3 to 7.6 TB/s.  A single small product is latency: 1 x 2048 x 7168 takes
+// 6.4 us, of which a launch is 3.9, and each wave's seven steps come two at a time.
 
 #include "fp8_matmul.hpp"
 #include "launch.hpp"
@@ -217,7 +221,8 @@ hipError_t launch(const Fp8Matmul &a, hipStream_t stream)
 //     8 .. 16   7.1 13.3 25          8.1 13.5 23          11.3 13.5 23
 //    32         8.2 15.8 38          10.6 13.8 26         14.7  -   25
 //    64        12.0 23.3 52          15.1 17.5 38         23.2 25.6 30
-// (T one less than needed for 33 x 4097: 257 workgroups of 16 rows 16.0, 129 of 32 12.6.)
+// Just past a full turn, 33 tokens and 4097 rows, fp32: 257 workgroups of 16 rows take 16.0
+// us, 129 of 32 rows 12.6.
 template <bool kMX, int kRagged, int T>
 hipError_t pick_rows(const Fp8Matmul &a, hipStream_t stream)
 {

@@ -588,9 +588,8 @@ mxq_status mxq_rmsnorm_backward(const mxq_rmsnorm_backward_args *args, void *str
  *       transposed gradient [out, tokens] and w = the transposed input [in,
  *       tokens], both from mxq_quantize_colwise_t, y is a linear layer's weight
  *       gradient [groups, out, in].
- * At most 65535 groups, and what one launch holds: below 2^28 columns for a few tokens,
- * below 2^39 results for many (MXQ_ESIZE otherwise); offsets and groups are NULL
- * and 0 for the dense forms.
+ * At most 65535 groups, and below 2^29 columns for a few tokens (MXQ_ESIZE otherwise);
+ * offsets and groups are NULL and 0 for the dense forms.
  * NaN codes and scales reach the sums they belong to.  The order of summation
  * depends on shapes alone; sums of MXFP8 are kept in the matrix cores, whose
  * fp32 additions cut off what they cannot hold (block-FP8: within 128 k).
