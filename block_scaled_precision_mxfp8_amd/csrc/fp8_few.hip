@@ -34,8 +34,10 @@ __global__ __launch_bounds__(W * 64) void few_kernel(Fp8Matmul a)
     constexpr int kSlot = kLoads * 1024;
     static_assert((D - 1) * kLoads < 64, "what vmcnt counts");
     constexpr int kOut = R * 16;                 // columns of y
+    static_assert(128 % kOut == 0, "in one tile of block-FP8's scales");
     constexpr int kRing = W * D * kSlot, kJoin = W * T * 16 * kOut * 4;
-    __shared__ __align__(1024) uint8_t lds[kRing > kJoin ? kRing : kJoin];
+    constexpr int kFar = kMX ? 0 : W * 4;        // a word of each wave
+    __shared__ __align__(1024) uint8_t lds[kRing > kJoin + kFar ? kRing : kJoin + kFar];
 
     int group = 0;
     int32_t row0 = blockIdx.y * (T * 16), row_end = min(row0 + T * 16, a.m);
@@ -80,15 +82,28 @@ __global__ __launch_bounds__(W * 64) void few_kernel(Fp8Matmul a)
         const uint4 v = bytes16_of(row, (s + 4 * g) * 4, kMX ? a.k / 32 : steps * 4);
         d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
     };
+    // Block-FP8: two scales within 2^-63 .. 2^63 have a product in fp32; are there others?
+    // Zeros (all there is behind the last step) have one too.
+    uint32_t least = ~0u, most = 0;
+    auto note = [&](const uint32_t(&d)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            least = min(least, (d[i] << 1) - 1u);
+            most = max(most, d[i] << 1);
+        }
+    };
     auto load_scales = [&](int32_t s) {
 #pragma unroll
-        for (int t = 0; t < T; ++t)
+        for (int t = 0; t < T; ++t) {
             load4(sx[t], a.sx, (int64_t)(row0 + min(t * 16 + p, xlast)) * a.ld_sx, s);
+            if constexpr (!kMX) note(sx[t]);
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int c = col0 + min(r * 16 + p, wlast);
             load4(sw[r], a.sw, (kRagged == kRows ? group * a.sw_stride : 0) + (int64_t)(kMX ? c : c / 128) * a.ld_sw, s);
         }
+        if constexpr (!kMX) note(sw[0]);  // that of all rows here
     };
 
     f32x4 acc[R][T];
@@ -186,6 +201,8 @@ __global__ __launch_bounds__(W * 64) void few_kernel(Fp8Matmul a)
     // -- join the waves: column p is a token, rows 4 g .. are columns of y
     __syncthreads();
     float *join_at = reinterpret_cast<float *>(lds);
+    uint32_t *far_at = reinterpret_cast<uint32_t *>(lds + kJoin);
+    if constexpr (!kMX) far_at[wave] = wave_any(least < (64u << 24) - 1u || most > (190u << 24));
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -197,8 +214,23 @@ __global__ __launch_bounds__(W * 64) void few_kernel(Fp8Matmul a)
         float v = join_at[e];
 #pragma unroll
         for (int i = 1; i < W; ++i) v += join_at[i * T * 16 * kOut + e];
-        if (t <= xlast && c <= wlast)
-            store_product(a.y, (int64_t)(row0 + t) * a.ldy + col0 + c, v, a.out_f32 != 0);
+        if (t > xlast || c > wlast) continue;
+        if constexpr (!kMX) {
+            if (unsure(v) >= kUnsure) {
+                uint32_t any = 0;
+#pragma unroll
+                for (int i = 0; i < W; ++i) any |= far_at[i];
+                const float *sxr = static_cast<const float *>(a.sx) + (int64_t)(row0 + t) * a.ld_sx;
+                const float *swr = static_cast<const float *>(a.sw) + (kRagged == kRows ? group * a.sw_stride : 0) +
+                                   (int64_t)((col0 + c) / 128) * a.ld_sw;
+                for (int32_t i = any ? 0 : steps; i < steps; ++i)
+                    if (odd_pair(__float_as_uint(sxr[i]), __float_as_uint(swr[i]))) {
+                        v = block_product_again(x + (int64_t)t * a.ldx, sxr, w + (int64_t)c * a.ldw, swr, a.k);
+                        break;
+                    }
+            }
+        }
+        store_product(a.y, (int64_t)(row0 + t) * a.ldy + col0 + c, v, a.out_f32 != 0);
     }
 }
 

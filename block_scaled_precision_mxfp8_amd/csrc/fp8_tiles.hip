@@ -428,6 +428,43 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
         __builtin_amdgcn_wave_barrier();
         const int32_t trow = row0 + (wt * CT + c) * 32;
         const int rows = min(32, row_end - trow);
+        if constexpr (!kMX) {
+            uint32_t worst = 0;
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) worst = max(worst, unsure(acc[r][c][i]));
+            const uint64_t look = __builtin_amdgcn_ballot_w64(worst >= kUnsure && p < rows && cols > 0);
+            if (look) {  // lane (p, h) looks through every other four of token p's scales
+                const float *sx = static_cast<const float *>(a.sx) + (int64_t)trow * a.ld_sx;
+                const float *sw = static_cast<const float *>(a.sw) + (kRagged == kRows ? group * a.sw_stride : 0) +
+                                  (int64_t)(wcol / 128) * a.ld_sw;
+                bool odd = false;
+                if ((look >> p | look >> (p + 32)) & 1) {
+#pragma unroll 4
+                    for (int32_t i = h * 16; i < steps * 4; i += 32) {
+                        const uint4 u = bytes16_of(reinterpret_cast<const uint8_t *>(sx + p * a.ld_sx), i, steps * 4);
+                        const uint4 v = bytes16_of(reinterpret_cast<const uint8_t *>(sw), i, steps * 4);
+                        odd |= odd_pair(u.x, v.x) || odd_pair(u.y, v.y) || odd_pair(u.z, v.z) || odd_pair(u.w, v.w);
+                    }
+                }
+                const uint64_t found = __builtin_amdgcn_ballot_w64(odd);
+                for (uint32_t left = (uint32_t)found | (uint32_t)(found >> 32); left; left &= left - 1) {
+                    const int tr = __builtin_ctz(left);
+                    for (int tc = lane; tc < cols; tc += 64) {
+                        const int byte = tc * kSize;
+                        uint8_t *at = mine + tr * kRow + (((byte >> 4) ^ (tr & 7)) << 4) + (byte & 15);
+                        const float v = kExact ? *reinterpret_cast<const float *>(at)
+                                               : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(at) << 16);
+                        if (unsure(v) < kUnsure) continue;
+                        const uint8_t *w = a.w + (kRagged == kRows ? group * a.w_stride : 0) + (int64_t)(wcol + tc) * a.ldw;
+                        const uint8_t *x = a.x + (int64_t)(trow + tr) * a.ldx;
+                        store_product(at, 0, block_product_again(x, sx + tr * a.ld_sx, w, sw, a.k), kExact);
+                    }
+                }
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
         if (wide) {
 #pragma unroll
             for (int i = 0; i < 32 / kRowsAt; ++i) {
