@@ -134,7 +134,7 @@ __global__ __launch_bounds__(W * 64) void few_kernel(Fp8Matmul a)
             for (int t = 0; t < T; ++t)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    decode16(bb[t][i], b[t][i], kMX ? e8m0_to_f32((cx[t] >> (8 * (2 * i + (g >> 1)))) & 0xFF) : 1.0f);
+                    decode16(bb[t][i], b[t][i], kMX ? lifted((cx[t] >> (8 * (2 * i + (g >> 1)))) & 0xFF) : 1.0f);
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -142,8 +142,8 @@ __global__ __launch_bounds__(W * 64) void few_kernel(Fp8Matmul a)
             const uint4 w1 = *reinterpret_cast<const uint4 *>(slot + r * 2048 + at1);
             if constexpr (kExact) {
                 bf16x8 ww[2][2];
-                decode16(ww[0], w0, kMX ? e8m0_to_f32((cw[r] >> (8 * (g >> 1))) & 0xFF) : 1.0f);
-                decode16(ww[1], w1, kMX ? e8m0_to_f32((cw[r] >> (8 * (2 + (g >> 1)))) & 0xFF) : 1.0f);
+                decode16(ww[0], w0, kMX ? lifted((cw[r] >> (8 * (g >> 1))) & 0xFF) : 1.0f);
+                decode16(ww[1], w1, kMX ? lifted((cw[r] >> (8 * (2 + (g >> 1)))) & 0xFF) : 1.0f);
 #pragma unroll
                 for (int t = 0; t < T; ++t) {
                     f32x4 q = kMX ? acc[r][t] : f32x4{0.f, 0.f, 0.f, 0.f};
@@ -229,6 +229,13 @@ __global__ __launch_bounds__(W * 64) void few_kernel(Fp8Matmul a)
                         break;
                     }
             }
+        }
+        if constexpr (kMX && kExact) {
+            v *= kLowered;
+            if (!__builtin_isfinite(v))
+                v = mx_product_again(v, x + (int64_t)t * a.ldx, static_cast<const uint8_t *>(a.sx) + (int64_t)(row0 + t) * a.ld_sx,
+                                     w + (int64_t)c * a.ldw, static_cast<const uint8_t *>(a.sw) +
+                                         (kRagged == kRows ? group * a.sw_stride : 0) + (int64_t)(col0 + c) * a.ld_sw, a.k);
         }
         store_product(a.y, (int64_t)(row0 + t) * a.ldy + col0 + c, v, a.out_f32 != 0);
     }

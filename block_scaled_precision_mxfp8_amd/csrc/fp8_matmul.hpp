@@ -111,7 +111,8 @@ __device__ __forceinline__ i32x8 join(uint4 a, uint4 b)
     return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 }
 
-// 16 codes times a power of two (1 or an MXFP8 scale) as bf16: exact wherever bf16 holds the value.
+// 16 codes times a power of two (1 or a lifted MXFP8 scale) as bf16: exact wherever bf16 holds
+// the value.  An infinite scale makes NaN of every code, 0 too.
 __device__ __forceinline__ void decode16(bf16x8 (&d)[2], uint4 q, float scale)
 {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -188,6 +189,60 @@ __device__ __forceinline__ float block_product_again(const uint8_t *x, const flo
             for (int j = 0; j < 16; ++j) part += (float)p[j / 8][j % 8] * (float)q[j / 8][j % 8];  // exact: four bits each
         }
         sum += part * ((double)sx[i] * (double)sw[i]);
+    }
+    return (float)sum;
+}
+
+// MXFP8 results in fp32: with both operands lifted by 2^10, codes are normal numbers of bf16
+// under every byte up to 236, so nothing is lost at that end, and sums come out 2^20 times
+// themselves.  At the other end codes become infinite (bytes above 236, where they are not 0
+// or the lifted scale is infinite) or sums do (of 2^108 and more): all of it ends in a
+// result that is not finite, which is then worked out again unless a scale of NaN is why.
+constexpr uint32_t kLift = 10;
+constexpr float kLowered = 0x1p-20f;
+__device__ __forceinline__ float lifted(uint32_t byte)
+{
+    return __uint_as_float(min(byte + kLift, 255u) << 23);
+}
+
+// Whether one of n scale bytes is NaN's.
+__device__ __forceinline__ bool nan_scale(const uint8_t *s, int32_t n)
+{
+    for (int32_t at = 0; at < n; at += 16) {
+        const uint4 v = bytes16_of(s, at, n);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) found |= (((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & w[i] & 0x80808080u) != 0;
+        if (found) return true;
+    }
+    return false;
+}
+
+// A result v that is not finite, of k values whose first scales are at sx and sw.
+__device__ __forceinline__ float mx_product_again(float v, const uint8_t *x, const uint8_t *sx, const uint8_t *w,
+                                                  const uint8_t *sw, int32_t k)
+{
+    const int32_t groups = (k + 31) / 32;
+    if (nan_scale(sx, groups) || nan_scale(sw, groups)) return __builtin_nanf("");
+    bool large = false;  // else a code is NaN
+#pragma unroll 1
+    for (int32_t i = 0; i < groups; ++i)
+        large |= max(sx[i], sw[i]) > 236 || sx[i] + sw[i] > 254 + 60;  // 2^22 products below 2^18 each
+    if (!large) return v;
+    double sum = 0;
+#pragma unroll 1  // little code, as above
+    for (int32_t at = 0; at < k; at += 16) {
+        auto load = [&](const uint8_t *row) {
+            return at + 16 <= k ? *reinterpret_cast<const uint4 *>(row + at) : first_bytes(row + at, k - at);
+        };
+        bf16x8 p[2], q[2];
+        decode16(p, load(x), 1.0f);
+        decode16(q, load(w), 1.0f);
+        double part = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part += (float)p[j / 8][j % 8] * (float)q[j / 8][j % 8];
+        sum += __builtin_ldexp(part, sx[at / 32] + sw[at / 32] - 254);
     }
     return (float)sum;
 }

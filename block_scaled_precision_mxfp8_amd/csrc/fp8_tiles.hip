@@ -254,11 +254,11 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
                     bf16x8 b[CT][2];
 #pragma unroll
                     for (int c = 0; c < CT; ++c)
-                        decode16(b[c], piece(stage, (wt * CT + c) * 32, i), e8m0_to_f32((sx[c] >> (8 * i)) & 0xFF));
+                        decode16(b[c], piece(stage, (wt * CT + c) * 32, i), lifted((sx[c] >> (8 * i)) & 0xFF));
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
                         bf16x8 w[2];
-                        decode16(w, piece(stage, BM + (wn * RT + r) * 32, i), e8m0_to_f32((sr[r] >> (8 * i)) & 0xFF));
+                        decode16(w, piece(stage, BM + (wn * RT + r) * 32, i), lifted((sr[r] >> (8 * i)) & 0xFF));
 #pragma unroll
                         for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -419,15 +419,43 @@ __global__ __launch_bounds__(WT *WN * 64, 2) void tile_kernel(Fp8Matmul a, TileG
                 const int byte = (r * 32 + 8 * i + 4 * h) * kSize;
                 uint8_t *to = mine + p * kRow + (((byte >> 4) ^ (p & 7)) << 4) + (byte & 15);
                 const f32x16 &v = acc[r][c];
-                if constexpr (kExact)
-                    *reinterpret_cast<f32x4 *>(to) = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-                else
+                if constexpr (kExact) {
+                    constexpr float f = kMX ? kLowered : 1.0f;
+                    *reinterpret_cast<f32x4 *>(to) = f32x4{v[4 * i] * f, v[4 * i + 1] * f, v[4 * i + 2] * f, v[4 * i + 3] * f};
+                } else {
                     *reinterpret_cast<uint2 *>(to) = make_uint2(bf16x2_rne(v[4 * i], v[4 * i + 1]),
                                                                 bf16x2_rne(v[4 * i + 2], v[4 * i + 3]));
+                }
             }
         __builtin_amdgcn_wave_barrier();
         const int32_t trow = row0 + (wt * CT + c) * 32;
         const int rows = min(32, row_end - trow);
+        if constexpr (kMX && kExact) {
+            static_assert(kCols == 64, "a lane has a column");
+            uint32_t worst = 0;
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) worst = max(worst, __float_as_uint(acc[r][c][i]) << 1);
+            const uint64_t look = __builtin_amdgcn_ballot_w64(worst >= 0xFF000000u && p < rows && cols > 0);
+            if (look) {  // tokens and columns with a scale of NaN stay as they are
+                const uint8_t *sx = static_cast<const uint8_t *>(a.sx) + (int64_t)trow * a.ld_sx + k0 / 32;
+                const int64_t col = min(wcol + lane, col_end - 1);
+                const uint8_t *w = a.w + (kRagged == kRows ? group * a.w_stride : 0) + col * a.ldw + k0;
+                const uint8_t *sw = static_cast<const uint8_t *>(a.sw) + (kRagged == kRows ? group * a.sw_stride : 0) +
+                                    col * a.ld_sw + k0 / 32;
+                const int32_t groups = (k1 - k0 + 31) / 32;
+                const bool in = lane < cols && !nan_scale(sw, groups);
+                const uint64_t found = look & ~__builtin_amdgcn_ballot_w64(p < rows && nan_scale(sx + p * a.ld_sx, groups));
+                for (uint32_t left = (uint32_t)found | (uint32_t)(found >> 32); left; left &= left - 1) {
+                    const int tr = __builtin_ctz(left);
+                    float *at = reinterpret_cast<float *>(mine + tr * kRow + (((lane >> 2) ^ (tr & 7)) << 4) + (lane & 3) * 4);
+                    if (in && !__builtin_isfinite(*at))
+                        *at = mx_product_again(*at, a.x + (int64_t)(trow + tr) * a.ldx + k0, sx + tr * a.ld_sx, w, sw, k1 - k0);
+                }
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
         if constexpr (!kMX) {
             uint32_t worst = 0;
 #pragma unroll

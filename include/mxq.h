@@ -590,9 +590,10 @@ mxq_status mxq_rmsnorm_backward(const mxq_rmsnorm_backward_args *args, void *str
  *       gradient [groups, out, in].
  * At most 65535 groups, and below 2^29 columns for a few tokens (MXQ_ESIZE otherwise);
  * offsets and groups are NULL and 0 for the dense forms.
- * NaN codes and scales reach the sums they belong to.  Block-FP8 scales may be of any
- * size: results that the product of two of them would spoil by leaving fp32 are worked
- * out one at a time, which takes long.  The order of summation otherwise
+ * NaN codes and scales reach the sums they belong to.  Scales may be of any size: results
+ * that the product of two block-FP8 scales would spoil by leaving fp32, or (in fp32)
+ * MXFP8 scales above byte 236, are worked out one at a time, which takes long.  The
+ * order of summation otherwise
  * depends on shapes alone; sums of MXFP8 are kept in the matrix cores, whose
  * fp32 additions cut off what they cannot hold (block-FP8: within 128 k).
  */
