@@ -267,9 +267,10 @@ hipError_t pick_rows(const Fp8Matmul &a, hipStream_t stream)
 {
     const int64_t at_once = (int64_t)a.n * (kRagged == kRows ? a.groups : 1);
     if (at_once <= 16 * 256) return launch<kMX, kRagged, 1, T, 8, 2>(a, stream);
-    if (T == 1 || at_once <= 32 * 256 || kRagged == kRows)
-        return launch<kMX, kRagged, 2, T, 4, T == 1 ? 3 : 2>(a, stream);
-    return launch<kMX, kRagged, 4, T, 4, 2>(a, stream);
+    if constexpr (T > 1 && kRagged == kDense) {
+        if (at_once > 32 * 256) return launch<kMX, kRagged, 4, T, 4, 2>(a, stream);
+    }
+    return launch<kMX, kRagged, 2, T, 4, T == 1 ? 3 : 2>(a, stream);
 }
 
 template <bool kMX, int kRagged>
