@@ -9,7 +9,8 @@
 // quantizer by that rounding.  Gradient, u = h * r, g = dy * weight:
 //   dx = r * (g - u * mean(g * u)) + dh,  dweight = sum over the rows of dy * u
 // (the quantizer counts as the identity).  Sums are of 8 values of a lane in fp32, then
-// over lanes and waves in a fixed order, in fp64 for the norm and fp32 for the gradient.
+// over lanes and waves in a fixed order, in fp64 for the norm and fp32 for the gradient;
+// rows whose squares leave fp32 (below 2^-45 or from 2^62 on) are summed in fp64 throughout.
 //
 // Bound by bytes: the norm reads 4 and writes 3 for a value (h, q), the gradient reads 6
 // and writes 2.  So a row is read once and stays in registers from the sum to the
@@ -111,6 +112,7 @@ __global__ __launch_bounds__(kWaves < 4 ? 256 : kWaves * 64, 7) void rmsnorm_ker
     const bool live = row < a.rows;
     uint4 v[kVecs];
     double sum = 0;
+    bool far = false;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         const int64_t col = (int64_t)(i * kWaves * 64 + in_row) * 8;
@@ -135,18 +137,39 @@ __global__ __launch_bounds__(kWaves < 4 ? 256 : kWaves * 64, 7) void rmsnorm_ker
 #pragma unroll
         for (int j = 0; j < 8; ++j) s = __builtin_fmaf(f.f[j], f.f[j], s);
         sum += s;
+        far |= live && col < a.cols && !(s >= 0x1p-90f && s < __builtin_inff());
+    }
+    if (wave_any(far)) {  // squares that leave fp32
+        sum = 0;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const Row8 f = floats(v[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = __builtin_fma((double)f.f[j], (double)f.f[j], sum);
+        }
     }
     // r is held in two floats and r * weight too: y is rounded about once, so that few
     // codes and hardly a scale fall to the other side of a border.
-    const double root = inverse_root(row_sum<kWaves>(sum, red, 0) / (double)a.cols + (double)a.eps);
+    double root = inverse_root(row_sum<kWaves>(sum, red, 0) / (double)a.cols + (double)a.eps);
+    if (a.rstd && live && in_row == 0) a.rstd[row] = (float)root;
+    // A root past 2^60 either way hands its power of two to the values, which it brings near 1:
+    // so neither it nor its product with a weight leaves fp32.
+    int lift = 0;
+    if (wave_any(root > 0 && root < __builtin_inf() && !(root >= 0x1p-60 && root <= 0x1p60))) {
+        lift = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_exp(root));  // a wave has one row
+        root = __builtin_amdgcn_ldexp(root, -lift);
+    }
     const float r = (float)root, r_low = r < __builtin_inff() ? (float)(root - (double)r) : 0.f;
-    if (a.rstd && live && in_row == 0) a.rstd[row] = r;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         const int64_t col = (int64_t)(i * kWaves * 64 + in_row) * 8;
         if (i * kWaves * 512 >= a.cols) break;
         const bool in = live && col < a.cols;
         Row8 y = floats(v[i]);
+        if (lift != 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y.f[j] = __builtin_amdgcn_ldexpf(y.f[j], lift);
+        }
         const Row8 w = in ? weights8<kWeightF32>(a.weight, col) : Row8{};
         uint32_t m = 0;
 #pragma unroll
@@ -166,7 +189,7 @@ __global__ __launch_bounds__(kWaves < 4 ? 256 : kWaves * 64, 7) void rmsnorm_ker
             // on a border: then it is worked out again, seldom and in few registers.
             auto rest = [&](int j) {  // above 0: the magnitude of value j is larger than y has it
                 const uint32_t pair = j < 2 ? v[i].x : j < 4 ? v[i].y : j < 6 ? v[i].z : v[i].w;
-                const float x = j & 1 ? bf16hi_to_f32(pair) : bf16lo_to_f32(pair);
+                const float x = __builtin_amdgcn_ldexpf(j & 1 ? bf16hi_to_f32(pair) : bf16lo_to_f32(pair), lift);
                 const float wj = kWeightF32 ? static_cast<const float *>(a.weight)[col + j]
                                             : bf16lo_to_f32(static_cast<const uint16_t *>(a.weight)[col + j]);
                 const float t = r * wj, low = __builtin_fmaf(r, wj, -t) + r_low * wj;

@@ -506,8 +506,9 @@ mxq_status nvfp4_matvec(const uint16_t *x, int64_t tokens, int64_t ldx, const ui
  *   rstd    optional fp32 [rows]: r
  * x, residual, weight, h and y are 16-byte aligned.  Shape: cols a multiple of 8
  * (blockfp8) or 32, at most 16384 (MXQ_ESIZE).  Squares are summed in fp32, eight at a
- * time, then in fp64: values of 2^62 make the sum infinite, and y zero.  cols == 0
- * writes nothing, rstd neither.
+ * time, then in fp64; in fp64 from the first in rows whose squares leave fp32, so x may
+ * be of any size.  rstd is infinite where r is 2^128 or more.  cols == 0 writes nothing,
+ * rstd neither.
  */
 typedef struct mxq_rmsnorm_args {
     const uint16_t *x, *residual;
