@@ -15,8 +15,11 @@
 // v_mfma_f32_16x16x32_bf16, eight bytes of a lane at a time.
 //
 // Bound by the weights' bytes where there are many: 512 rows of 128 groups of 2048 x 7168
-// 246 to 258 us, 7.3 to 7.6 TB/s.  A single small product is latency: 1 x 2048 x 7168 takes
-// 6.4 us, of which a launch is 3.9, and each wave's seven steps come two at a time.
+// 246 to 261 us, 7.2 to 7.6 TB/s.  A single small product is latency: 1 x 2048 x 7168 takes
+// 6.6 us, of which a launch is 3.9.  Then a wave waits for the scales of its tokens and
+// weight rows, R + T loads one after the other (each is shifted, and so waited for, before
+// the next; scale rows of less than 16 bytes come byte by byte), before it asks for the
+// first weights; and its seven steps come two at a time.
 
 #include "fp8_matmul.hpp"
 #include "launch.hpp"
@@ -255,13 +258,14 @@ hipError_t launch(const Fp8Matmul &a, hipStream_t stream)
 
 // Rows to a workgroup (R x 16) so that every CU has one and none has a second turn for
 // a few rows; with few rows more waves cut the contraction, and two workgroups fit a CU
-// where LDS allows.  us for n x k = 4096 x 7168, 8192 x 8192, 16384 x 7168 on MI355X:
+// where LDS allows.  us of a call, block-FP8, for n x k = 4096 x 7168, 8192 x 8192, 16384 x
+// 7168 on MI355X (below about 10 it is the host's time that counts):
 //   tokens      R 1, 8 waves         R 2, 4 waves         R 4, 4 waves
-//     8 .. 16   7.1 13.3 25          8.1 13.5 23          11.3 13.5 23
-//    32         8.2 15.8 38          10.6 13.8 26         14.7  -   25
-//    64        12.0 23.3 52          15.1 17.5 38         23.2 25.6 30
-// Just past a full turn, 33 tokens and 4097 rows, fp32: 257 workgroups of 16 rows take 16.0
-// us, 129 of 32 rows 12.6.
+//        16      9.4 12.7 25.5        9.1 13.3 22.9         -
+//        32      9.6 16.5 38.7       11.0 14.3 26.8       15.2 16.6 25.4
+//        64     13.1 24.1 53.3       16.5 17.9 39.2       24.3 26.3 31.0
+// Just past a full turn, 33 tokens and 4097 rows: 257 workgroups of 16 rows take 17.5 us (fp32
+// MXFP8 19.4), 129 of 32 rows 13.6 (15.7); 4096 rows in 256 workgroups of 16 take 10.6 (11.8).
 template <bool kMX, int kRagged, int T>
 hipError_t pick_rows(const Fp8Matmul &a, hipStream_t stream)
 {
@@ -277,7 +281,8 @@ template <bool kMX, int kRagged>
 hipError_t pick(const Fp8Matmul &a, int tokens, hipStream_t stream)
 {
     if constexpr (kRagged == kRows) {
-        // 512 rows of 128 groups: T 1 294 us, 2 292; longer groups take more tiles
+        // 1, 4 and 16 rows a group, 128 groups of 2048 x 7168, us: T 1 172 255 424, 2 178 260 404;
+        // longer groups take more tiles
         return tokens <= 16 ? pick_rows<kMX, kRagged, 2>(a, stream) : pick_rows<kMX, kRagged, 4>(a, stream);
     } else {
         if (tokens <= 16) return pick_rows<kMX, kRagged, 1>(a, stream);

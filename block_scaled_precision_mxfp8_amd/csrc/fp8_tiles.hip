@@ -22,14 +22,15 @@
 // bf16, without loss, and v_mfma_f32_32x32x16_bf16 multiplies: 1.5e-7, at half the rate.
 //
 // Bound, where the contraction is long, by the matrix cores: 4096 x 8192 x 8192 MXFP8
-// 234 us (2.35 PFLOP/s; the matrix cores busy 80 % of it at 2.1 GHz), 8192 x 7168 x 7168
-// block-FP8 428 us (1.97 PFLOP/s; 3.5 rounds of tiles cost as much as 4, and the FMAs
-// with the scales run beside the products only in part).  So LDS is filled straight from
-// memory, two steps deep, and what a step has to read from it is read under the last
+// 238 us (2.31 PFLOP/s; the matrix cores busy 80 % of it at 2.1 GHz), 8192 x 7168 x 7168
+// block-FP8 432 to 455 us (1.85 to 1.95 PFLOP/s; 3.5 rounds of tiles cost as much as 4, and
+// the FMAs with the scales run beside the products only in part).  So LDS is filled straight
+// from memory, two steps deep, and what a step has to read from it is read under the last
 // step's products.  Where it is short, by what does not overlap in a CU that holds one
 // tile: 16384 tokens of 32 groups as the contraction of 2048 x 7168 weight gradients,
-// four steps a tile, take 485 us, of which the stores alone are 181, the steps 240
-// and the start of 7168 workgroups 106.
+// four steps a tile, take 481 to 517 us, of which the stores alone are 181, the steps 240
+// and the start of 7168 workgroups 106 (its second step is asked for only when the first is
+// there: the scales loaded between the two are waited for).
 
 #include "fp8_matmul.hpp"
 #include "launch.hpp"
@@ -544,9 +545,13 @@ template <bool kMX, int kRagged>
 hipError_t pick(const Fp8Matmul &a, hipStream_t stream)
 {
     if (a.out_f32) return launch<kMX, true, kRagged, 2, 2, 2, 2>(a, stream);
-    // 256 x 256 tiles, one to a CU, or 128 x 128, two.  A round of 256 large ones takes
-    // 1.8 us a step (k = 7168: 101 us), as many small ones 0.85, 512 of them 1.3 (73 us): so
-    // much work is four rounds of these, or three quarters of a round of the large.
+    // 256 x 256 tiles, one to a CU, or 128 x 128, two.  us at k = 7168, MXFP8 (block-FP8 takes
+    // 3 to 15 % more), by the number of large tiles that there would be:
+    //             64    128    160    176    208    256    512
+    //   large     97     96     90     94     95    100    208
+    //   small     52     75    117    114    119    132    283
+    // So the large ones are ahead from somewhere between 128 and 160 on; 192 is later than
+    // that.  Rows of several groups are counted as if they were one group's.
     const int64_t big = (int64_t)((a.m + 255) / 256) * ((a.n + 255) / 256) * (kRagged == kContraction ? a.groups : 1);
     if (big >= 192) return launch<kMX, false, kRagged, 4, 2, 2, 4>(a, stream);
     return launch<kMX, false, kRagged, 2, 2, 2, 2>(a, stream);
@@ -557,9 +562,18 @@ hipError_t pick(const Fp8Matmul &a, hipStream_t stream)
 hipError_t launch_fp8_matmul(bool mx, int ragged, const Fp8Matmul &a, hipStream_t stream)
 {
     // Up to 64 tokens the weights are the work; and while a product has few tiles, more
-    // and smaller workgroups are ahead although they read the weights again for every 64.
+    // and smaller workgroups are ahead although they read the weights again for every 64.  us
+    // at k = 7168, block-FP8:
+    //   tokens x n      128 x 8192  128 x 16384  256 x 4096  256 x 7168  512 x 2048  1024 x 2048
+    //   few tokens'         33          55           44          62          44           81
+    //   tiles               48          66           47          47          47           48
     if (ragged == kDense && (a.m <= 64 || (int64_t)((a.m + 63) / 64) * a.n <= 16384))
         return launch_fp8_few(mx, ragged, a.m, a, stream);
+    // Rows a group on average, us, 32 groups of 2048 x 7168 in block-FP8 and 128 of 2048 x 2048 in
+    // MXFP8, whose short contraction the tiles are ahead with from few rows on:
+    //                   8    16    32    48          8    16    32    48
+    //   few tokens'    85    97   165   190        135   158   322   385
+    //   tiles         139   144   149   147        115   119   145   173
     if (ragged == kRows && a.m <= (int64_t)32 * a.groups && a.m / 32 + a.groups < 65535)
         return launch_fp8_few(mx, ragged, (a.m - 1) / a.groups + 1, a, stream);
     if (mx)

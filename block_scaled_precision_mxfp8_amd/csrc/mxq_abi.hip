@@ -252,7 +252,7 @@ bool kv_shape_ok(int32_t heads, int32_t dim, int32_t page)
            mxq::Kv4Geom{0, 0, heads, dim, page}.page_bytes() <= 0x7FFFFFFF;
 }
 
-// Checks a cache description (its data pointer only when it has pages).
+// What the two norms share.
 mxq_status rmsnorm(bool mx, const mxq_rmsnorm_args *p, void *stream)
 {
     if (!p || p->reserved != 0) return MXQ_EINVAL;
@@ -341,6 +341,7 @@ mxq_status fp8_matmul(bool mx, int ragged, const mxq_matmul_args *p, void *strea
     return e == hipErrorInvalidConfiguration ? MXQ_ESIZE : from_hip(e);
 }
 
+// Checks a cache description (its data pointer only when it has pages).
 mxq_status check_kv(const mxq_kv_cache *c, mxq::Kv4Geom &geo)
 {
     if (!c || c->pages < 0 || c->reserved != 0) return MXQ_EINVAL;

@@ -15,9 +15,12 @@
 // Bound by bytes: the norm reads 4 and writes 3 for a value (h, q), the gradient reads 6
 // and writes 2.  So a row is read once and stays in registers from the sum to the
 // output, up to 32 values a lane, and as few waves share it as hold it: their sum costs a
-// barrier.  Rows stream past the caches (non-temporal): 16384 x 7168 with residual 145 us
-// (5.7 TB/s) where ordinary accesses took 157, the gradient 165 (5.7 TB/s) where 183.
-// One row is a chain of latencies, 6.1 us: two loads, two sums over lanes and a barrier.
+// barrier.  Rows stream past the caches (non-temporal): 16384 x 7168 with residual 146 us
+// (5.7 TB/s) where ordinary accesses took 157, the gradient 164 (5.7 TB/s) where 183; of what
+// that does to the kernel that reads them next, and to small batches, nothing is measured.
+// One row is a chain of latencies, 6.2 us of which a launch is 3.9: four pieces of x and the
+// residual, each pair waited for before the next is asked for, the sum over lanes and a
+// barrier, then four pieces of the weight, again one after the other.
 
 #include "launch.hpp"
 #include "mxq_device.hpp"
@@ -101,7 +104,8 @@ __device__ __forceinline__ uint32_t signs_of(const float *f)
 
 // kWaves waves on a row; a workgroup has at least four.  Seven waves to a SIMD: with
 // registers for five or six 160 us (16384 x 7168, ordinary accesses), for seven 157, for
-// eight, spilling, 178; held to five or four workgroups a CU 156 and 173 where 146.
+// eight, spilling, 178; held to five or four workgroups a CU 156 and 173 where 146.  (fp32
+// weights with MXFP8 spill one or two registers of it: 150 us.)
 template <bool kMX, int kWaves, bool kWeightF32>
 __global__ __launch_bounds__(kWaves < 4 ? 256 : kWaves * 64, 7) void rmsnorm_kernel(RmsNorm a)
 {
