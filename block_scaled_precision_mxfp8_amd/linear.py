@@ -129,7 +129,9 @@ def blockfp8_matmul(q: torch.Tensor, S: torch.Tensor, wq: torch.Tensor, wS: torc
     """Tokens times the transpose of block-FP8 weights: q uint8 [m, k] with S
     float32 [m, ceil(k/128)] (``blockfp8_quantize_1x128``, ``rmsnorm_blockfp8``), wq
     uint8 [n, k] with wS float32 [ceil(n/128), ceil(k/128)] (``blockfp8_quantize``):
-    [m, n], summed in fp32, bf16 or fp32.  k is a multiple of 16; codes may also be
+    [m, n], summed in fp32, bf16 or fp32.  Of 8 neighbouring products bf16 results
+    drop what lies below 2^-13 of the largest, far below their rounding unless a sum
+    cancels; fp32 results, which with many tokens take about twice the time, drop nothing.  k is a multiple of 16; codes may also be
     float8_e4m3fn.  For the gradient of the tokens pass the quantized gradient and
     wq.t().contiguous(), wS.t().contiguous()."""
     return _matmul("blockfp8_matmul", False, q, S, wq, wS, out_dtype, out)
@@ -140,7 +142,8 @@ def mxfp8_matmul(q: torch.Tensor, scale: torch.Tensor, wq: torch.Tensor, wscale:
     """Tokens times the transpose of MXFP8 weights: q uint8 [m, k] with scale
     uint8 [m, k/32], wq uint8 [n, k] with wscale uint8 [n, k/32] (``quantize_rowwise``,
     or of transposed matrices ``quantize_colwise_t``): [m, n], summed in fp32, bf16 or
-    fp32.  k is a multiple of 32; codes and scales may also have their float8 types."""
+    fp32, as blockfp8_matmul has them.  k is a multiple of 32; codes and scales may also
+    have their float8 types."""
     return _matmul("mxq_matmul", True, q, scale, wq, wscale, out_dtype, out)
 
 

@@ -528,7 +528,7 @@ mxq_status mxq_rmsnorm(const mxq_rmsnorm_args *args, void *stream);
 
 /*
  * The gradient of that norm, the quantizer counted as the identity: with u = h * r
- * and g = dy * weight,
+ * and g = dy * weight, in fp32,
  *   dx = bf16_RNE(r * (g - u * mean(g * u)) + dh),  dweight = sum over rows of dy * u
  *   dy, h, dh  [rows, cols] bf16, row strides in elements (multiples of 8); dh, the
  *           gradient that reaches h past the norm, may be NULL; 16-byte aligned
@@ -558,7 +558,7 @@ mxq_status mxq_rmsnorm_backward(const mxq_rmsnorm_backward_args *args, void *str
 
 /*
  * Products of 8-bit tokens with 8-bit weights (blockfp8_*: block-FP8, mxq_*:
- * MXFP8), summed in fp32, rounded once:
+ * MXFP8), summed in fp32:
  *   y[i, j] = sum_k x[i, k] w[j, k]
  * x [m, k] and w [n, k] are E4M3 codes, row strides ldx and ldw bytes, 16-byte
  * aligned, strides multiples of 16 and at most 2^22.  Scales, row strides
@@ -571,7 +571,13 @@ mxq_status mxq_rmsnorm_backward(const mxq_rmsnorm_backward_args *args, void *str
  * y [m, n] is bf16, or fp32 when out_fp32 != 0, row stride ldy elements, aligned
  * to its element (rows of 16-byte multiples are written faster).  k % 16 == 0
  * (block-FP8) or k % 32 == 0 (MXFP8), MXQ_ESHAPE otherwise; any m, n >= 0; k == 0
- * writes zeros.  The gradient of x is the product of y's gradient, quantized
+ * writes zeros.
+ * Results in fp32 are sums of exact products, off by some 2^-22 of their norm.
+ * Results in bf16 are rounded once from sums made with the 8-bit matrix instructions,
+ * which of the products of 8 neighbouring k drop what lies below 2^-13 of the largest:
+ * 5e-5 of a sum's norm, a thirtieth of the rounding, but an absolute error that a sum
+ * which cancels keeps.
+ * The gradient of x is the product of y's gradient, quantized
  * along n, with the transposed weights: 128 x 128 tiles and their scales may be
  * transposed as they are.
  *
@@ -589,14 +595,16 @@ mxq_status mxq_rmsnorm_backward(const mxq_rmsnorm_backward_args *args, void *str
  *       transposed gradient [out, tokens] and w = the transposed input [in,
  *       tokens], both from mxq_quantize_colwise_t, y is a linear layer's weight
  *       gradient [groups, out, in].
- * At most 65535 groups, and below 2^29 columns for a few tokens (MXQ_ESIZE otherwise);
- * offsets and groups are NULL and 0 for the dense forms.
+ * At most 65535 groups, 2^31 - 256 rows or columns, and what a launch of 2^32 - 1 threads
+ * reaches: 2^29 columns for a few tokens, tiles of 128 x 128 (256 threads) or 256 x 256
+ * (512) for many, one more row of tiles for each group (MXQ_ESIZE otherwise); offsets
+ * and groups are NULL and 0 for the dense forms.
  * NaN codes and scales reach the sums they belong to.  Scales may be of any size: results
  * that the product of two block-FP8 scales would spoil by leaving fp32, or (in fp32)
  * MXFP8 scales above byte 236, are worked out one at a time, which takes long.  The
- * order of summation otherwise
- * depends on shapes alone; sums of MXFP8 are kept in the matrix cores, whose
- * fp32 additions cut off what they cannot hold (block-FP8: within 128 k).
+ * order of summation otherwise depends on shapes alone; sums of MXFP8 are kept in the
+ * matrix cores, whose fp32 additions cut off what they cannot hold (block-FP8: within
+ * 128 k).
  */
 typedef struct mxq_matmul_args {
     const uint8_t *x;
