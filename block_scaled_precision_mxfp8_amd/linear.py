@@ -131,9 +131,10 @@ def blockfp8_matmul(q: torch.Tensor, S: torch.Tensor, wq: torch.Tensor, wS: torc
     uint8 [n, k] with wS float32 [ceil(n/128), ceil(k/128)] (``blockfp8_quantize``):
     [m, n], summed in fp32, bf16 or fp32.  Of 8 neighbouring products bf16 results
     drop what lies below 2^-13 of the largest, far below their rounding unless a sum
-    cancels; fp32 results, which with many tokens take about twice the time, drop nothing.  k is a multiple of 16; codes may also be
-    float8_e4m3fn.  For the gradient of the tokens pass the quantized gradient and
-    wq.t().contiguous(), wS.t().contiguous()."""
+    cancels; fp32 results, which with many tokens take about twice the time, drop
+    nothing.  k is a multiple of 16; codes may also be float8_e4m3fn.  For the gradient
+    of the tokens pass the quantized gradient and wq.t().contiguous(),
+    wS.t().contiguous()."""
     return _matmul("blockfp8_matmul", False, q, S, wq, wS, out_dtype, out)
 
 
