@@ -106,3 +106,17 @@ def test_nan_scales_with_codes_of_one_sign_and_none(gpu, codes, m, n, out):
     bad[:, [9, n - 1]] = True
     assert torch.equal(torch.isnan(y), bad)
     assert (y[~bad] == (96 if 0 not in codes else 0)).all()
+
+
+@BOTH
+@SIZES
+def test_large_results(gpu, m, n, out):
+    """Sums of 2^100 to 2^124, which in fp32 lie past what the lifted operands hold."""
+    g = ref.generator(m)
+    q, w = ref.codes(g, m, 96), ref.codes(g, n, 96)
+    s = torch.randint(160, 185, (m, 3), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.randint(160, 170, (n, 3), generator=g, device="cuda", dtype=torch.uint8)
+    y = gpu.mxfp8_matmul(q, s, w, ws, out_dtype=out)
+    rows = torch.arange(min(m, 70), device="cuda")
+    ref.check(y[rows], ref.mx(q[rows], s[rows]), ref.mx(w, ws))
+    assert y.abs().max() > 2.0 ** 108
