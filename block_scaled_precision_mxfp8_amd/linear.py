@@ -22,6 +22,8 @@ _MATMUL = struct.Struct("@PPqqPPqqqqPqqPqqqiiq")
 _RMSNORM = struct.Struct("@PPPPPPPPqqqqfiq")
 _RMSNORM_BACKWARD = struct.Struct("@PPPPPPPPNqqqqqii")
 
+_MOST_LD = 1 << 22  # bytes between rows of codes
+
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
@@ -38,7 +40,8 @@ def _call(fn: str, device: torch.device, args: bytes):
 
 
 def _codes(t, what: str, dims: int, device=None) -> torch.Tensor:
-    """E4M3 codes with a unit last stride and 16-byte aligned rows (a copy if they have none)."""
+    """E4M3 codes with a unit last stride and 16-byte aligned rows no further apart than the
+    kernels' 32-bit offsets reach (a copy if they have none)."""
     if not isinstance(t, torch.Tensor) or (t.dtype is not torch.uint8 and t.dtype is not torch.float8_e4m3fn):
         raise TypeError(f"{what} must be a uint8 or float8_e4m3fn tensor")
     if device is None:
@@ -49,7 +52,7 @@ def _codes(t, what: str, dims: int, device=None) -> torch.Tensor:
     stride = t.stride()
     if len(stride) != dims:
         raise ValueError(f"{what} must have {dims} dimensions")
-    if stride[-1] == 1 and not t.data_ptr() & 15 and not stride[-2] & 15 and stride[-2] >= t.shape[-1] \
+    if stride[-1] == 1 and not t.data_ptr() & 15 and not stride[-2] & 15 and t.shape[-1] <= stride[-2] <= _MOST_LD \
             and (dims == 2 or not stride[0] & 15):
         return t
     if t.shape[-1] % 16 == 0:
